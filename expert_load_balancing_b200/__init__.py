@@ -10,6 +10,8 @@ from . import binding  # noqa: F401  (loads the library lazily, on first call)
 from .binding import (  # noqa: F401
     KolibriError,
     expert_ffn_workspace,
+    kolibri_balance_loss,
+    kolibri_balance_loss_grad,
     kolibri_device_status,
     kolibri_eqb_bf16_bias,
     kolibri_eqb_bf16_digit,
@@ -28,6 +30,8 @@ from .binding import (  # noqa: F401
     kolibri_expert_permute_noalloc,
     kolibri_intervention_rate,
     kolibri_lei_inject,
+    kolibri_rms_norm,
+    kolibri_rms_norm_grad,
     kolibri_route_and_balance,
     kolibri_router_forward,
     kolibri_router_forward_eqb,

@@ -31,6 +31,10 @@ KOLIBRI_ERR_DEVICE = 6
 KOLIBRI_OP_PERMUTE = 1
 KOLIBRI_OP_EQB = 2
 KOLIBRI_OP_EQB_BF16 = 3
+KOLIBRI_TYPE_BF16 = 0
+KOLIBRI_TYPE_F32 = 1
+KOLIBRI_SCORE_SIGMOID = 0
+KOLIBRI_SCORE_SOFTMAX = 1
 # size of the library-held scratch of kolibri_expert_permute_noalloc (the header's macro)
 KOLIBRI_NOALLOC_SCRATCH_BYTES = 2 << 20
 
@@ -73,6 +77,16 @@ SIGNATURES = {
     "kolibri_expert_gate_up": (ctypes.c_int, [_P, _I64, _P, _I32, _P, _P, _I32, _I32, _P]),
     "kolibri_expert_down": (ctypes.c_int, [_P, _I64, _P, _I32, _P, _P, _I32, _I32, _P]),
     "kolibri_expert_combine": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _I32, _P, _P]),
+    "kolibri_balance_loss_workspace_size": (_SZ, [_I64, _I32, _I32]),
+    "kolibri_balance_loss": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _I32, _I32, ctypes.c_double, _P, _I32,
+                                            _P, _P, _P, _P, _P, _SZ, _P]),
+    "kolibri_balance_loss_grad": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _I32, _I32, ctypes.c_double, _P,
+                                                 _I32, _P, _P]),
+    "kolibri_rms_norm": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _I32, ctypes.c_float, _I64, _I32, _P, _P, _P, _P,
+                                        _P]),
+    "kolibri_rms_norm_grad_workspace_size": (_SZ, [_I64, _I32]),
+    "kolibri_rms_norm_grad": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _I32, ctypes.c_float, _P, _I64, _I32, _P, _P,
+                                             _P, _SZ, _P]),
     "kolibri_device_status": (ctypes.c_int, [_P]),
     "kolibri_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint64, _P]),
 }
@@ -655,3 +669,155 @@ def kolibri_expert_combine(y_perm: torch.Tensor, y_shared: torch.Tensor | None, 
            load().kolibri_expert_combine(_ptr(y_perm), _ptr(y_shared), _ptr(inv), _ptr(gates), N, d, K,
                                          _ptr(y), _stream(stream)))
     return y
+
+
+# ------------------------------------------------- the norm and the balance loss
+
+_TYPE = {torch.bfloat16: KOLIBRI_TYPE_BF16, torch.float32: KOLIBRI_TYPE_F32}
+
+
+def _on_current(t, name):
+    """The library launches on the current device: refuse a tensor of another one."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device, got {t.device}")
+
+
+def _need_all(dev, *args):
+    """_need for (tensor, dtype, shape, name) in turn, with one device for all; None tensors pass."""
+    for t, dtype, shape, name in args:
+        if t is None:
+            continue
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                             f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _type_of(t, name):
+    code = _TYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return code
+
+
+def kolibri_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, res: torch.Tensor | None = None,
+                     res_out: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                     y8: torch.Tensor | None = None, scales: torch.Tensor | None = None, want_y: bool = True,
+                     want_fp8: bool = False, stream=None):
+    """h = x + res and its root-mean-square norm times weight [d]: x, res [N, d] bf16 or fp32 each.
+
+    Returns (res_out like res or None, y [N, d] bf16 or None, y8 [N, d] float8_e4m3fn or None,
+    scales [N, ceil(d/128)] fp32 or None); y8 * scales is the norm again.  res_out may be res (in place)."""
+    N, d = x.shape
+    dev = x.device
+    _on_current(x, "x")
+    xt, wt = _type_of(x, "x"), _type_of(weight, "weight")
+    rt = 0 if res is None else _type_of(res, "res")
+    if res is None:
+        if res_out is not None:
+            raise ValueError("res_out: needs res")
+    elif res_out is None:
+        res_out = torch.empty_like(res)
+    if y is None and want_y:
+        y = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+    groups = (d + 127) // 128
+    if y8 is None and want_fp8:
+        y8 = torch.empty((N, d), dtype=torch.float8_e4m3fn, device=dev)
+    if scales is None and y8 is not None:
+        scales = torch.empty((N, groups), dtype=torch.float32, device=dev)
+    _need_all(dev, (x, x.dtype, (N, d), "x"), (weight, weight.dtype, (d,), "weight"),
+              (res, None if res is None else res.dtype, (N, d), "res"),
+              (res_out, None if res is None else res.dtype, (N, d), "res_out"), (y, torch.bfloat16, (N, d), "y"),
+              (y8, torch.float8_e4m3fn, (N, d), "y8"), (scales, torch.float32, (N, groups), "scales"))
+    _check("kolibri_rms_norm",
+           load().kolibri_rms_norm(_ptr(x), xt, _ptr(res), rt, _ptr(weight), wt, eps, N, d, _ptr(res_out), _ptr(y),
+                                   _ptr(y8), _ptr(scales), _stream(stream)))
+    return res_out, y, y8, scales
+
+
+def kolibri_rms_norm_grad(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, eps: float,
+                          gres: torch.Tensor | None = None, gx: torch.Tensor | None = None,
+                          gweight: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                          want_gweight: bool = True, stream=None):
+    """The gradient of kolibri_rms_norm at h = x + res (its res_out): gy [N, d] is dL/dy, gres [N, d] dL/dres_out.
+
+    Returns (gx [N, d] of h's type: the gradient of x and of res alike, gweight [d] fp32 or None)."""
+    N, d = h.shape
+    dev = h.device
+    _on_current(h, "h")
+    ht, gt, wt = _type_of(h, "h"), _type_of(gy, "gy"), _type_of(weight, "weight")
+    if gx is None:
+        gx = torch.empty_like(h)
+    if gweight is None and want_gweight:
+        gweight = torch.empty((d,), dtype=torch.float32, device=dev)
+    if ws is None and gweight is not None:
+        n = int(load().kolibri_rms_norm_grad_workspace_size(N, d))
+        ws = torch.empty((max(n, 1),), dtype=torch.uint8, device=dev)
+    _need_all(dev, (h, h.dtype, (N, d), "h"), (gy, gy.dtype, (N, d), "gy"), (weight, weight.dtype, (d,), "weight"),
+              (gres, h.dtype, (N, d), "gres"), (gx, h.dtype, (N, d), "gx"), (gweight, torch.float32, (d,), "gweight"),
+              (ws, torch.uint8, (0 if ws is None else ws.numel(),), "ws"))
+    _check("kolibri_rms_norm_grad",
+           load().kolibri_rms_norm_grad(_ptr(gy), gt, _ptr(h), ht, _ptr(weight), wt, eps, _ptr(gres), N, d, _ptr(gx),
+                                        _ptr(gweight), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+    return gx, gweight
+
+
+def kolibri_balance_loss(z: torch.Tensor, ids: torch.Tensor, lam: float, seq_offsets: torch.Tensor | None = None,
+                         score: int = KOLIBRI_SCORE_SIGMOID, grad_loss: torch.Tensor | None = None,
+                         gz: torch.Tensor | None = None, want_gz: bool = False, accumulate: bool = False,
+                         loss: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                         prob: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """The auxiliary balance loss of the routing ids [N, K] on the logits z [N, E], per sequence of seq_offsets [S+1].
+
+    Returns (loss [S] fp32, counts [S, E] int32, prob [S, E] fp32, gz [N, E] fp32 or None).  With want_gz (or gz) the
+    same pass writes the gradient of sum_s grad_loss[s] loss[s], or adds it to gz with accumulate."""
+    N, E = z.shape
+    K = ids.shape[1]
+    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    dev = z.device
+    _on_current(z, "z")
+    if gz is None and want_gz:
+        if accumulate:
+            raise ValueError("gz: accumulate needs the gradient to add to")
+        gz = torch.empty((N, E), dtype=torch.float32, device=dev)
+    if loss is None:
+        loss = torch.empty((S,), dtype=torch.float32, device=dev)
+    if counts is None:
+        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    if prob is None:
+        prob = torch.empty((S, E), dtype=torch.float32, device=dev)
+    if ws is None:
+        n = int(load().kolibri_balance_loss_workspace_size(N, E, S))
+        ws = torch.empty((max(n, 1),), dtype=torch.uint8, device=dev)
+    _need_all(dev, (z, torch.float32, (N, E), "z"), (ids, torch.int32, (N, K), "ids"),
+              (seq_offsets, torch.int64, (S + 1,), "seq_offsets"), (grad_loss, torch.float32, (S,), "grad_loss"),
+              (gz, torch.float32, (N, E), "gz"), (loss, torch.float32, (S,), "loss"),
+              (counts, torch.int32, (S, E), "counts"), (prob, torch.float32, (S, E), "prob"),
+              (ws, torch.uint8, (ws.numel(),), "ws"))
+    _check("kolibri_balance_loss",
+           load().kolibri_balance_loss(_ptr(z), _ptr(ids), _ptr(seq_offsets), N, E, K, S, score, lam, _ptr(grad_loss),
+                                       1 if accumulate else 0, _ptr(loss), _ptr(counts), _ptr(prob), _ptr(gz), _ptr(ws),
+                                       ws.numel(), _stream(stream)))
+    return loss, counts, prob, gz
+
+
+def kolibri_balance_loss_grad(z: torch.Tensor, counts: torch.Tensor, K: int, lam: float,
+                              seq_offsets: torch.Tensor | None = None, score: int = KOLIBRI_SCORE_SIGMOID,
+                              grad_loss: torch.Tensor | None = None, gz: torch.Tensor | None = None,
+                              accumulate: bool = False, stream=None) -> torch.Tensor:
+    """The gradient of kolibri_balance_loss from the counts [S, E] it wrote: gz [N, E] fp32, added to with accumulate."""
+    N, E = z.shape
+    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    dev = z.device
+    _on_current(z, "z")
+    if gz is None:
+        if accumulate:
+            raise ValueError("gz: accumulate needs the gradient to add to")
+        gz = torch.empty((N, E), dtype=torch.float32, device=dev)
+    _need_all(dev, (z, torch.float32, (N, E), "z"), (counts, torch.int32, (S, E), "counts"),
+              (seq_offsets, torch.int64, (S + 1,), "seq_offsets"), (grad_loss, torch.float32, (S,), "grad_loss"),
+              (gz, torch.float32, (N, E), "gz"))
+    _check("kolibri_balance_loss_grad",
+           load().kolibri_balance_loss_grad(_ptr(z), _ptr(counts), _ptr(seq_offsets), N, E, K, S, score, lam,
+                                            _ptr(grad_loss), 1 if accumulate else 0, _ptr(gz), _stream(stream)))
+    return gz

@@ -1,6 +1,8 @@
 // api.cu -- the extern "C" boundary declared in include/kolibri_router.h:
 // argument validation, workspace sizing and the device status word.
+#include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "launch.h"
 #include "common.cuh"
@@ -414,6 +416,100 @@ kolibri_status kolibri_expert_combine(const float* y_perm, const float* y_shared
                                          static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+kolibri_status check_balance_loss(int64_t N, int32_t E, int32_t K, int32_t S, const int64_t* seq, int32_t score,
+                                  int32_t accumulate, double lambda) {
+  const kolibri_status st = check_ek(N, E, K);
+  if (st != KOLIBRI_OK) return st;
+  if (S < 1 || (!seq && S != 1)) return KOLIBRI_ERR_INVALID_ARG;
+  if (score != KOLIBRI_SCORE_SIGMOID && score != KOLIBRI_SCORE_SOFTMAX) return KOLIBRI_ERR_INVALID_ARG;
+  if ((accumulate != 0 && accumulate != 1) || !std::isfinite(lambda)) return KOLIBRI_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(S) * E >= (static_cast<int64_t>(1) << 31)) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
+  return KOLIBRI_OK;
+}
+
+bool type_ok(int32_t t) { return t == KOLIBRI_TYPE_BF16 || t == KOLIBRI_TYPE_F32; }
+
+kolibri_status check_norm(int64_t N, int32_t d, float eps) {
+  if (N < 1 || d < 1 || !(eps >= 0.0f) || !std::isfinite(eps)) return KOLIBRI_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > 16384 || N >= (static_cast<int64_t>(1) << 31)) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
+  return KOLIBRI_OK;
+}
+
+}  // namespace
+
+size_t kolibri_balance_loss_workspace_size(int64_t N, int32_t E, int32_t S) {
+  if (N < 1 || E < 1 || E > KOLIBRI_MAX_EXPERTS || S < 1 ||
+      static_cast<int64_t>(S) * E >= (static_cast<int64_t>(1) << 31))
+    return 0;
+  return balance_loss_ws_bytes(N, E, S);
+}
+
+kolibri_status kolibri_balance_loss(const float* z, const int32_t* ids, const int64_t* seq_offsets, int64_t N,
+                                    int32_t E, int32_t K, int32_t S, int32_t score, double lambda,
+                                    const float* grad_loss, int32_t accumulate, float* loss, int32_t* counts,
+                                    float* prob, float* gz, void* ws, size_t ws_bytes, void* stream) {
+  const kolibri_status st = check_balance_loss(N, E, K, S, seq_offsets, score, accumulate, lambda);
+  if (st != KOLIBRI_OK) return st;
+  if (!z || !ids || !loss || !counts || !prob || !ws) return KOLIBRI_ERR_INVALID_ARG;
+  for (const void* q : {static_cast<const void*>(z), static_cast<const void*>(ids),
+                        static_cast<const void*>(seq_offsets), static_cast<const void*>(grad_loss),
+                        static_cast<const void*>(loss), static_cast<const void*>(counts),
+                        static_cast<const void*>(prob), static_cast<const void*>(gz), static_cast<const void*>(ws)})
+    if (!aligned16(q)) return KOLIBRI_ERR_INVALID_ARG;
+  if (ws_bytes < balance_loss_ws_bytes(N, E, S)) return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
+  return from_cuda(launch_balance_loss(z, ids, seq_offsets, N, E, K, S, score, lambda, grad_loss, accumulate, loss,
+                                       counts, prob, gz, ws, static_cast<cudaStream_t>(stream)));
+}
+
+kolibri_status kolibri_balance_loss_grad(const float* z, const int32_t* counts, const int64_t* seq_offsets,
+                                         int64_t N, int32_t E, int32_t K, int32_t S, int32_t score, double lambda,
+                                         const float* grad_loss, int32_t accumulate, float* gz, void* stream) {
+  const kolibri_status st = check_balance_loss(N, E, K, S, seq_offsets, score, accumulate, lambda);
+  if (st != KOLIBRI_OK) return st;
+  if (!z || !counts || !gz) return KOLIBRI_ERR_INVALID_ARG;
+  if (!aligned16(z) || !aligned16(counts) || !aligned16(seq_offsets) || !aligned16(grad_loss) || !aligned16(gz))
+    return KOLIBRI_ERR_INVALID_ARG;
+  return from_cuda(launch_balance_loss_grad(z, counts, seq_offsets, N, E, K, S, score, lambda, grad_loss, accumulate,
+                                            gz, static_cast<cudaStream_t>(stream)));
+}
+
+kolibri_status kolibri_rms_norm(const void* x, int32_t x_type, const void* res, int32_t res_type,
+                                const void* weight, int32_t weight_type, float eps, int64_t N, int32_t d,
+                                void* res_out, void* y, void* y8, float* scales, void* stream) {
+  const kolibri_status st = check_norm(N, d, eps);
+  if (st != KOLIBRI_OK) return st;
+  if (!type_ok(x_type) || !type_ok(weight_type) || (res && !type_ok(res_type))) return KOLIBRI_ERR_INVALID_ARG;
+  if (!x || !weight || (!y && !y8) || (y8 == nullptr) != (scales == nullptr) || (res_out && !res))
+    return KOLIBRI_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(res) || !aligned16(weight) || !aligned16(res_out) || !aligned16(y) ||
+      !aligned16(y8) || !aligned16(scales))
+    return KOLIBRI_ERR_INVALID_ARG;
+  return from_cuda(launch_rms_norm(x, x_type, res, res_type, weight, weight_type, eps, N, d, res_out, y, y8, scales,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+size_t kolibri_rms_norm_grad_workspace_size(int64_t N, int32_t d) {
+  return check_norm(N, d, 0.0f) == KOLIBRI_OK ? rms_norm_grad_ws_bytes(N, d) : 0;
+}
+
+kolibri_status kolibri_rms_norm_grad(const void* gy, int32_t gy_type, const void* h, int32_t h_type,
+                                     const void* weight, int32_t weight_type, float eps, const void* gres,
+                                     int64_t N, int32_t d, void* gx, float* gweight, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  const kolibri_status st = check_norm(N, d, eps);
+  if (st != KOLIBRI_OK) return st;
+  if (!type_ok(gy_type) || !type_ok(h_type) || !type_ok(weight_type)) return KOLIBRI_ERR_INVALID_ARG;
+  if (!gy || !h || !weight || !gx || (gweight && !ws)) return KOLIBRI_ERR_INVALID_ARG;
+  if (!aligned16(gy) || !aligned16(h) || !aligned16(weight) || !aligned16(gres) || !aligned16(gx) ||
+      !aligned16(gweight) || !aligned16(ws))
+    return KOLIBRI_ERR_INVALID_ARG;
+  if (gweight && ws_bytes < rms_norm_grad_ws_bytes(N, d)) return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
+  return from_cuda(launch_rms_norm_grad(gy, gy_type, h, h_type, weight, weight_type, eps, gres, N, d, gx, gweight,
+                                        ws, static_cast<cudaStream_t>(stream)));
+}
+
 kolibri_status kolibri_selftest_bounded_wait(uint64_t limit_ns, void* stream) {
   if (limit_ns < 1000ull || limit_ns > 1000000000ull) return KOLIBRI_ERR_INVALID_ARG;
   bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns);
@@ -426,7 +522,7 @@ kolibri_status kolibri_device_status(void* stream) {
   const unsigned v = status_take_api() | status_take_eqb() | status_take_noalloc() |
                      status_take_permute() | status_take_route() | status_take_logits() |
                      status_take_forward() | status_take_balance() | status_take_small() |
-                     status_take_experts() | status_take_decode();
+                     status_take_experts() | status_take_decode() | status_take_balance_loss();
   if (v & kStatusReadFailed) return KOLIBRI_ERR_CUDA;
   if (v & kStatusTimeout) return KOLIBRI_ERR_TIMEOUT;
   if (v & kStatusBadInput) return KOLIBRI_ERR_DEVICE;

@@ -1,0 +1,407 @@
+// balance_loss.cu -- the auxiliary balance loss over the router's scores, the
+// per-expert counts it weighs them with, and its gradient to the logits.
+//
+// The loss that "Kolibri Pre-Training from Scratch" 6.2 and 7 set Exact
+// Quantile Balancing against.  Per sequence of T tokens (or once over a batch):
+//
+//   p_te = q_te / sum_j q_tj       q = exp(z) (softmax) or sigma(z) (the router's gate)
+//   f_e  = E c_e / (K T)           c_e = slots of the sequence routed to e
+//   P_e  = mean_t p_te,            L = lambda sum_e f_e P_e
+//   dL/dz_te = lambda / T p_te (f_e - sum_j f_j p_tj) (1 - sigma(z_te) with sigmoid scores)
+//
+// The counts carry no gradient (they come from the selection).  As sum_j p_tj
+// = 1, f enters as f - 1 throughout, which keeps the difference in the bracket
+// exact to fp32 when the loads are nearly even, and L = lambda (1 + mean_t
+// dot_t) with dot_t = sum_j (f_j - 1) p_tj, the sum that the gradient needs
+// anyway.
+//
+// The gradient needs f, which comes from the ids alone, and not P: so the
+// counts are formed first (a read of the ids) and ONE pass over Z then forms
+// P, L and dL/dZ.  Bound by HBM: 4 E bytes of Z read and, with the gradient,
+// 4 E bytes written per token.
+//
+// Sums over tokens: fp32 per warp over the rows of one block, then the blocks'
+// shares in fp64 in a fixed order; counts are integers.  Nothing depends on
+// the order in which blocks run.
+//
+// A block's chunk of rows may hold several sequences and a sequence may span
+// several chunks.  The (chunk c, sequence s) pairs that meet form a staircase
+// on which c + s never repeats, so the share of a pair is kept in row c + s of
+// the workspace.
+#include "launch.h"
+#include "common.cuh"
+#include "pdl.cuh"
+
+namespace kolibri {
+
+namespace {
+
+constexpr int kLossWarps = 8;
+constexpr int kLossThreads = 32 * kLossWarps;
+constexpr int kLossBlocksPerSm = 4;
+constexpr int kMaxE = KOLIBRI_MAX_EXPERTS;
+
+// Sequence boundaries: seq[0..S] (or null: one sequence of all rows), cut to
+// [0, N] so that no index leaves the arrays whatever the caller wrote.
+struct Seqs {
+  const int64_t* seq;
+  int64_t N;
+  int S;
+  __device__ __forceinline__ int64_t at(int s) const {
+    if (!seq) return s == 0 ? 0 : N;
+    const int64_t v = seq[s];
+    return v < 0 ? 0 : (v > N ? N : v);
+  }
+  // the last s < S with at(s) <= row, or 0
+  __device__ __forceinline__ int find(int64_t row) const {
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (at(mid) <= row) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+// counts [S][E] += the slots of this block's rows.  counts is zero on entry.
+__global__ void __launch_bounds__(kLossThreads) seq_count_kernel(const int32_t* ids, Seqs q, int E, int K,
+                                                                 int64_t chunk, int32_t* counts) {
+  __shared__ int32_t hist[kMaxE];
+  const int64_t r0 = blockIdx.x * chunk;
+  const int64_t r1 = r0 + chunk < q.N ? r0 + chunk : q.N;
+  for (int e = threadIdx.x; e < E; e += kLossThreads) hist[e] = 0;
+  if (blockIdx.x == 0 && q.seq)
+    for (int s = threadIdx.x; s <= q.S; s += kLossThreads) {
+      const int64_t v = q.seq[s];
+      if (v < 0 || v > q.N || (s > 0 && q.seq[s - 1] > v)) raise_status(kStatusBadInput);
+    }
+  __syncthreads();
+  for (int s = q.find(r0); s < q.S; ++s) {
+    const int64_t b = q.at(s), e_ = q.at(s + 1);
+    if (b >= r1) break;
+    const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
+    if (lo >= hi) continue;
+    for (int64_t j = lo * K + threadIdx.x; j < hi * K; j += kLossThreads) {
+      const int32_t e = ids[j];
+      if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+      else raise_status(kStatusBadInput);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kLossThreads) {
+      const int32_t c = hist[e];
+      if (c) {
+        atomicAdd(&counts[static_cast<int64_t>(s) * E + e], c);
+        hist[e] = 0;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+struct LossParams {
+  const float* z;
+  const int32_t* counts;    // [S, E]
+  const float* grad_loss;   // [S] or null (ones)
+  float* gz;                // [N, E]
+  float* part;              // [chunks + S][E]: sums of p
+  double* dots;             // [chunks + S]: sums of dot_t
+  Seqs q;
+  int64_t chunk;
+  int E, K;
+  int accumulate;
+  double lambda;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// e^x by the hardware's base-2 exponential: about 2^-22 + |x| 2^-24 relative,
+// far below the 2^-24 sqrt(T) of the sums it enters; e^-inf = 0.
+__device__ __forceinline__ float fast_exp(float x) { return __expf(x); }
+
+// A warp per row; lane l holds the float4s l, l + 32, ... (V of them) of the
+// row's E logits.
+//
+// Sigmoid scores are formed as q = 1 / (e^c + e^(c - z)) = e^-c sigma(z) with c
+// = min(max_j z_j, 0): the common factor keeps rows whose logits are all far
+// below zero from vanishing.  1 - sigma(z) = q e^(c - z) where sigma > 1/2 and
+// 1 - q e^c elsewhere, both free of cancellation.  A row without a finite
+// logit gives p = 0 and gradient 0.
+template <int V, bool kSoftmax, bool kProb, bool kGrad>
+__global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossParams p) {
+  __shared__ float psum[kProb ? kLossWarps * kMaxE : 1];
+  __shared__ double dsum[kLossWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int E4 = p.E >> 2;
+  const Seqs q = p.q;
+  const int64_t r0 = blockIdx.x * p.chunk;
+  const int64_t r1 = r0 + p.chunk < q.N ? r0 + p.chunk : q.N;
+  pdl_wait();          // the counts
+  if constexpr (kGrad) {
+    // rows of the chunk before the first and behind the last sequence have no gradient
+    if (!p.accumulate) {
+      const int64_t first = q.at(0), last = q.at(q.S);
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4* g4 = reinterpret_cast<float4*>(p.gz);
+      const int64_t a1 = first < r1 ? first : r1, b0 = last > r0 ? last : r0;
+      for (int64_t i = r0 * E4 + threadIdx.x; i < a1 * E4; i += kLossThreads) g4[i] = zero;
+      for (int64_t i = b0 * E4 + threadIdx.x; i < r1 * E4; i += kLossThreads) g4[i] = zero;
+    }
+  }
+  for (int s = q.find(r0); s < q.S; ++s) {
+    const int64_t b = q.at(s), e_ = q.at(s + 1);
+    if (b >= r1) break;
+    const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
+    if (lo >= hi) continue;
+    const double T = static_cast<double>(e_ - b);
+    const double to_f = static_cast<double>(p.E) / (static_cast<double>(p.K) * T);
+    float fr[4 * V], acc[4 * V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c4 = lane + 32 * j;
+      int4 c = make_int4(0, 0, 0, 0);
+      if (c4 < E4) c = reinterpret_cast<const int4*>(p.counts)[static_cast<int64_t>(s) * E4 + c4];
+      fr[4 * j + 0] = static_cast<float>(c.x * to_f - 1.0);
+      fr[4 * j + 1] = static_cast<float>(c.y * to_f - 1.0);
+      fr[4 * j + 2] = static_cast<float>(c.z * to_f - 1.0);
+      fr[4 * j + 3] = static_cast<float>(c.w * to_f - 1.0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * V; ++i) acc[i] = 0.0f;
+    float gscale = 0.0f;
+    if constexpr (kGrad)
+      gscale = static_cast<float>(p.lambda / T * (p.grad_loss ? static_cast<double>(p.grad_loss[s]) : 1.0));
+    double dot_sum = 0.0;
+    for (int64_t row = lo + warp; row < hi; row += kLossWarps) {
+      const float4* zr = reinterpret_cast<const float4*>(p.z) + row * E4;
+      float z[4 * V], u[4 * V];
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c4 = lane + 32 * j;
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (c4 < E4) v = __ldcs(zr + c4);
+        z[4 * j] = v.x; z[4 * j + 1] = v.y; z[4 * j + 2] = v.z; z[4 * j + 3] = v.w;
+        m = fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+      }
+      m = warp_max(m);
+      const bool none = m == -INFINITY;
+      float sum = 0.0f, dot = 0.0f, ec = 1.0f;
+      if constexpr (kSoftmax) {
+        const float c = none ? 0.0f : m;
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) {
+          z[i] = fast_exp(z[i] - c);
+          sum += z[i];
+          dot = fmaf(fr[i], z[i], dot);
+        }
+      } else {
+        const float c = none ? 0.0f : fminf(m, 0.0f);
+        ec = fast_exp(c);
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) {
+          u[i] = fast_exp(c - z[i]);
+          z[i] = __fdividef(1.0f, ec + u[i]);
+          sum += z[i];
+          dot = fmaf(fr[i], z[i], dot);
+        }
+      }
+      sum = warp_sum(sum);
+      dot = warp_sum(dot);
+      const float inv = none ? 0.0f : __fdividef(1.0f, sum);
+      dot = __fmul_rn(dot, inv);          // uncontracted: the same bits in every form of the pass
+      if constexpr (kProb) {
+        dot_sum += none ? -1.0f : dot;     // a row without p adds nothing to L
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
+      }
+      if constexpr (kGrad) {
+        const float k = gscale * inv;
+        float4* gr = reinterpret_cast<float4*>(p.gz) + row * E4;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int c4 = lane + 32 * j;
+          float o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int x = 4 * j + i;
+            o[i] = k * z[x] * (fr[x] - dot);
+            if constexpr (!kSoftmax) o[i] *= u[x] < ec ? z[x] * u[x] : fmaf(-z[x], ec, 1.0f);
+          }
+          if (c4 < E4) {
+            if (p.accumulate) {
+              const float4 old = gr[c4];
+              o[0] += old.x; o[1] += old.y; o[2] += old.z; o[3] += old.w;
+            }
+            __stcs(gr + c4, make_float4(o[0], o[1], o[2], o[3]));
+          }
+        }
+      }
+    }
+    if constexpr (kProb) {
+      const int64_t slot = blockIdx.x + s;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c4 = lane + 32 * j;
+        if (c4 < E4)
+          reinterpret_cast<float4*>(psum + warp * kMaxE)[c4] =
+              make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+      }
+      if (lane == 0) dsum[warp] = dot_sum;
+      __syncthreads();
+      for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kLossWarps; ++w) t += psum[w * kMaxE + e];
+        p.part[slot * p.E + e] = t;
+      }
+      if (threadIdx.x == 0) {
+        double t = 0.0;
+#pragma unroll
+        for (int w = 0; w < kLossWarps; ++w) t += dsum[w];
+        p.dots[slot] = t;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// prob[s][e] and loss[s] from the blocks' shares: a block per sequence and 32
+// experts, 16 shares at a time, fp64, fixed order.
+constexpr int kFinishRows = 16;
+__global__ void __launch_bounds__(32 * kFinishRows) balance_finish_kernel(const LossParams p, float* prob, float* loss) {
+  __shared__ double buf[kFinishRows][32];
+  pdl_wait();
+  const int tiles = (p.E + 31) / 32;
+  const int s = blockIdx.x / tiles, tile = blockIdx.x - s * tiles;
+  const int e = tile * 32 + threadIdx.x;
+  const int64_t b = p.q.at(s), en = p.q.at(s + 1);
+  const int64_t n = en > b ? en - b : 0;
+  const int64_t c0 = n ? b / p.chunk : 0, c1 = n ? (en - 1) / p.chunk + 1 : 0;   // chunks that hold rows of s
+  double t = 0.0;
+  if (e < p.E)
+#pragma unroll 4
+    for (int64_t c = c0 + threadIdx.y; c < c1; c += kFinishRows) t += p.part[(c + s) * p.E + e];
+  buf[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y == 0 && e < p.E) {
+    t = 0.0;
+#pragma unroll
+    for (int r = 0; r < kFinishRows; ++r) t += buf[r][threadIdx.x];
+    prob[static_cast<int64_t>(s) * p.E + e] = n ? static_cast<float>(t / static_cast<double>(n)) : 0.0f;
+  }
+  if (tile == 0) {
+    __syncthreads();
+    t = 0.0;
+    for (int64_t c = c0 + threadIdx.y * 32 + threadIdx.x; c < c1; c += 32 * kFinishRows) t += p.dots[c + s];
+    buf[threadIdx.y][threadIdx.x] = t;
+    __syncthreads();
+    if (threadIdx.y == 0) {
+      t = 0.0;
+#pragma unroll
+      for (int r = 0; r < kFinishRows; ++r) t += buf[r][threadIdx.x];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (threadIdx.x == 0) loss[s] = n ? static_cast<float>(p.lambda * (1.0 + t / static_cast<double>(n))) : 0.0f;
+    }
+  }
+}
+
+struct LossPlan {
+  int64_t chunk, chunks;
+};
+LossPlan loss_plan(int64_t N) {
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * kLossBlocksPerSm;
+  LossPlan lp;
+  lp.chunk = (N + most - 1) / most;
+  lp.chunk = (lp.chunk + kLossWarps - 1) / kLossWarps * kLossWarps;
+  lp.chunks = (N + lp.chunk - 1) / lp.chunk;
+  return lp;
+}
+
+template <int V, bool kSoftmax, bool kProb, bool kGrad>
+cudaError_t launch_loss_pass(const LossParams& p, int64_t chunks, cudaStream_t s) {
+  return launch_pdl(balance_loss_kernel<V, kSoftmax, kProb, kGrad>, dim3(static_cast<unsigned>(chunks)),
+                    dim3(kLossThreads), 0, s, dim3(0, 0, 0), p);
+}
+
+template <bool kProb, bool kGrad>
+cudaError_t launch_loss_v(const LossParams& p, int score, int64_t chunks, cudaStream_t s) {
+  const bool soft = score == KOLIBRI_SCORE_SOFTMAX;
+  switch ((p.E + 127) / 128) {
+    case 1: return soft ? launch_loss_pass<1, true, kProb, kGrad>(p, chunks, s) : launch_loss_pass<1, false, kProb, kGrad>(p, chunks, s);
+    case 2: return soft ? launch_loss_pass<2, true, kProb, kGrad>(p, chunks, s) : launch_loss_pass<2, false, kProb, kGrad>(p, chunks, s);
+    case 3: return soft ? launch_loss_pass<3, true, kProb, kGrad>(p, chunks, s) : launch_loss_pass<3, false, kProb, kGrad>(p, chunks, s);
+    default: return soft ? launch_loss_pass<4, true, kProb, kGrad>(p, chunks, s) : launch_loss_pass<4, false, kProb, kGrad>(p, chunks, s);
+  }
+}
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+size_t balance_loss_ws_bytes(int64_t N, int32_t E, int32_t S) {
+  const size_t rows = static_cast<size_t>(loss_plan(N).chunks) + S;
+  return round256(rows * E * sizeof(float)) + rows * sizeof(double);
+}
+
+cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_t* seq, int64_t N, int32_t E,
+                                int32_t K, int32_t S, int score, double lambda, const float* grad_loss,
+                                int accumulate, float* loss, int32_t* counts, float* prob, float* gz, void* ws,
+                                cudaStream_t s) {
+  const LossPlan lp = loss_plan(N);
+  LossParams p{};
+  p.z = z;
+  p.counts = counts;
+  p.grad_loss = grad_loss;
+  p.gz = gz;
+  p.part = static_cast<float*>(ws);
+  p.dots = reinterpret_cast<double*>(static_cast<char*>(ws) +
+                                     round256((static_cast<size_t>(lp.chunks) + S) * E * sizeof(float)));
+  p.q = Seqs{seq, N, S};
+  p.chunk = lp.chunk;
+  p.E = E;
+  p.K = K;
+  p.accumulate = accumulate;
+  p.lambda = lambda;
+  cudaError_t err = cudaMemsetAsync(counts, 0, sizeof(int32_t) * static_cast<size_t>(S) * E, s);
+  if (err != cudaSuccess) return err;
+  seq_count_kernel<<<static_cast<unsigned>(lp.chunks), kLossThreads, 0, s>>>(ids, p.q, E, K, lp.chunk, counts);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  err = gz ? launch_loss_v<true, true>(p, score, lp.chunks, s) : launch_loss_v<true, false>(p, score, lp.chunks, s);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(balance_finish_kernel, dim3(static_cast<unsigned>((E + 31) / 32) * S), dim3(32, kFinishRows), 0, s, dim3(0, 0, 0), p, prob,
+                    loss);
+}
+
+cudaError_t launch_balance_loss_grad(const float* z, const int32_t* counts, const int64_t* seq, int64_t N,
+                                     int32_t E, int32_t K, int32_t S, int score, double lambda,
+                                     const float* grad_loss, int accumulate, float* gz, cudaStream_t s) {
+  const LossPlan lp = loss_plan(N);
+  LossParams p{};
+  p.z = z;
+  p.counts = counts;
+  p.grad_loss = grad_loss;
+  p.gz = gz;
+  p.q = Seqs{seq, N, S};
+  p.chunk = lp.chunk;
+  p.E = E;
+  p.K = K;
+  p.accumulate = accumulate;
+  p.lambda = lambda;
+  return launch_loss_v<false, true>(p, score, lp.chunks, s);
+}
+
+KOLIBRI_DEFINE_STATUS_TAKE(status_take_balance_loss)
+
+}  // namespace kolibri

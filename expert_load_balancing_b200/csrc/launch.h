@@ -181,6 +181,26 @@ cudaError_t launch_score_grad(const float* z, const float* gs, int64_t n, float*
 cudaError_t launch_intervention(const float* z, const int32_t* ids, int64_t N, int32_t E, int32_t K,
                                 unsigned long long* total, double* rate, cudaStream_t s);
 
+// norm.cu: the norm in front of the router and its gradient.
+cudaError_t launch_rms_norm(const void* x, int x_type, const void* res, int res_type, const void* weight,
+                            int weight_type, float eps, int64_t N, int32_t d, void* res_out, void* y,
+                            void* y8, float* scales, cudaStream_t s);
+size_t rms_norm_grad_ws_bytes(int64_t N, int32_t d);
+cudaError_t launch_rms_norm_grad(const void* gy, int gy_type, const void* h, int h_type,
+                                 const void* weight, int weight_type, float eps, const void* gres,
+                                 int64_t N, int32_t d, void* gx, float* gweight, void* ws,
+                                 cudaStream_t s);
+
+// balance_loss.cu: the auxiliary balance loss, its counts and gradient.
+size_t balance_loss_ws_bytes(int64_t N, int32_t E, int32_t S);
+cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_t* seq, int64_t N, int32_t E,
+                                int32_t K, int32_t S, int score, double lambda, const float* grad_loss,
+                                int accumulate, float* loss, int32_t* counts, float* prob, float* gz, void* ws,
+                                cudaStream_t s);
+cudaError_t launch_balance_loss_grad(const float* z, const int32_t* counts, const int64_t* seq, int64_t N,
+                                     int32_t E, int32_t K, int32_t S, int score, double lambda,
+                                     const float* grad_loss, int accumulate, float* gz, cudaStream_t s);
+
 int device_sm_count();
 
 // Read and clear the status word of one translation unit (see common.cuh).
@@ -217,5 +237,6 @@ unsigned status_take_balance();
 unsigned status_take_small();
 unsigned status_take_experts();
 unsigned status_take_decode();
+unsigned status_take_balance_loss();
 
 }  // namespace kolibri

@@ -1,0 +1,406 @@
+// norm.cu -- the norm in front of the router: root-mean-square norm of the
+// residual stream with the residual's addition, a bf16 output for the router
+// and an 8-bit output with scales for the experts, and its gradient.
+//
+// "Kolibri 1 im Detail", routing and FP8 sections: the router takes bf16
+// tokens [N, 2560]; the experts' activations are E4M3 with one fp32 scale per
+// 1 x 128 group.
+//
+//   h = x + res                       fp32; res_out = h rounded once to res's type
+//   r = rsqrt(mean(h^2) + eps)        fp32, from the unrounded h
+//   y = h r g                         fp32; rounded once to bf16
+//   s = max(amax_group |y|, 1e-30) / 448,  y8 = e4m3(y 448 / amax)   from the fp32 y
+//
+// Bound by HBM: each input is read once and each output written once, the
+// row stays in registers between the sum of squares and the outputs.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "launch.h"
+#include "common.cuh"
+#include "pdl.cuh"
+
+namespace kolibri {
+
+namespace {
+
+constexpr int kVec = 8;                  // elements per thread and step: 16 bytes of bf16
+constexpr int kGroupVecs = 128 / kVec;   // threads of one 8-bit scale group
+constexpr int kMaxNormThreads = 1024;   // d = 16384 at two vecs per thread
+constexpr int kMaxNormWarps = kMaxNormThreads / 32;
+constexpr float kAmaxMin = 1e-30f;       // keeps the scale and its reciprocal normal numbers
+constexpr float kE4m3Max = 448.0f;
+
+struct Vec8 {
+  float v[kVec];
+};
+
+template <typename T>
+__device__ __forceinline__ Vec8 load8(const void* p, int64_t vec) {
+  Vec8 o;
+  if constexpr (sizeof(T) == 2) {
+    const uint4 u = reinterpret_cast<const uint4*>(p)[vec];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o.v[2 * i] = __uint_as_float(w[i] << 16);
+      o.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(p) + 2 * vec;
+    const float4 a = q[0], b = q[1];
+    o.v[0] = a.x; o.v[1] = a.y; o.v[2] = a.z; o.v[3] = a.w;
+    o.v[4] = b.x; o.v[5] = b.y; o.v[6] = b.z; o.v[7] = b.w;
+  }
+  return o;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(void* p, int64_t vec, const Vec8& a) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(a.v[2 * i], a.v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    reinterpret_cast<uint4*>(p)[vec] = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    float4* q = reinterpret_cast<float4*>(p) + 2 * vec;
+    q[0] = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
+    q[1] = make_float4(a.v[4], a.v[5], a.v[6], a.v[7]);
+  }
+}
+
+// The weight's eight entries of a vec, in fp32.
+__device__ __forceinline__ Vec8 load_weight(const void* g, int f32, int64_t vec) {
+  return f32 ? load8<float>(g, vec) : load8<__nv_bfloat16>(g, vec);
+}
+
+// Sums of NV values over the block, in a fixed order.  One barrier: `buf`
+// alternates between calls, so a slow warp may still read the other half.
+template <int NV>
+__device__ __forceinline__ void block_sums(float (&v)[NV], float* buf, int warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (warps == 1) return;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) buf[i * kMaxNormWarps + warp] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float s = 0.0f;
+    for (int w = 0; w < warps; ++w) s += buf[i * kMaxNormWarps + w];
+    v[i] = s;
+  }
+}
+
+struct NormParams {
+  const void* x;
+  const void* res;
+  const void* g;
+  void* res_out;
+  void* y;            // bf16, or null
+  uint8_t* y8;        // e4m3, or null
+  float* scales;      // [N, groups]
+  int64_t N;
+  int nvec;           // d / 8
+  int groups;         // ceil(d / 128)
+  int g_f32;
+  float inv_d, eps;
+};
+
+struct NoRes {};
+
+// A block per row and step; thread t holds the vecs t, t + T, ... of the row.
+// T is a multiple of 32, so a scale group is 16 neighbouring lanes.
+template <typename XT, typename RT, int C>
+__global__ void __launch_bounds__(C == 1 ? 512 : kMaxNormThreads) rms_norm_kernel(const NormParams p) {
+  constexpr bool kRes = !std::is_same<RT, NoRes>::value;
+  __shared__ float buf[2][kMaxNormWarps];
+  const int T = blockDim.x, warps = T >> 5;
+  Vec8 g[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int v = threadIdx.x + c * T;
+    if (v < p.nvec) g[c] = load_weight(p.g, p.g_f32, v);
+  }
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
+    const int64_t base = row * p.nvec;
+    Vec8 h[C];
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int v = threadIdx.x + c * T;
+      if (v < p.nvec) {
+        h[c] = load8<XT>(p.x, base + v);
+        if constexpr (kRes) {
+          const Vec8 r = load8<RT>(p.res, base + v);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) h[c].v[i] += r.v[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) h[c].v[i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) ss[0] = fmaf(h[c].v[i], h[c].v[i], ss[0]);
+      if constexpr (kRes) {
+        const int v = threadIdx.x + c * T;
+        if (p.res_out && v < p.nvec) store8<RT>(p.res_out, base + v, h[c]);
+      }
+    }
+    block_sums<1>(ss, buf[flip], warps);
+    const float r = rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int v = threadIdx.x + c * T;
+      const bool in = v < p.nvec;
+      Vec8 y;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) y.v[i] = in ? h[c].v[i] * r * g[c].v[i] : 0.0f;
+      if (p.y && in) store8<__nv_bfloat16>(p.y, base + v, y);
+      if (p.y8) {
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) a = fmaxf(a, fabsf(y.v[i]));
+#pragma unroll
+        for (int o = kGroupVecs / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        a = fmaxf(a, kAmaxMin);
+        const float q = __fdiv_rn(kE4m3Max, a);
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y.v[4 * i] * q, y.v[4 * i + 1] * q), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y.v[4 * i + 2] * q, y.v[4 * i + 3] * q), __NV_SATFINITE, __NV_E4M3);
+          w[i] = lo | (hi << 16);
+        }
+        if (in) {
+          reinterpret_cast<uint2*>(p.y8)[base + v] = make_uint2(w[0], w[1]);
+          if (v % kGroupVecs == 0) p.scales[row * p.groups + v / kGroupVecs] = __fdiv_rn(a, kE4m3Max);
+        }
+      }
+    }
+  }
+}
+
+// ---- gradient -------------------------------------------------------------
+//
+//   xh = h r, t = gy g:   gx = r (t - xh mean(t xh)) + gres
+//                            = r t - h r^3 (sum t h) / d + gres
+//   gg = sum over rows of gy xh
+//
+// Both row sums (h^2 and t h) are reduced together; the block's share of gg
+// stays in registers over its rows and goes to one row of the workspace, and
+// a second kernel adds those rows in a fixed order: no atomics, the same bits
+// on every run.
+
+struct NormGradParams {
+  const void* gy;
+  const void* h;
+  const void* g;
+  const void* gres;
+  void* gx;
+  float* part;        // [gridDim.x, d], or null: no weight gradient
+  int64_t N;
+  int nvec, g_f32;
+  float inv_d, eps;
+};
+
+template <typename GT, typename HT, int C>
+__global__ void __launch_bounds__(C == 1 ? 512 : kMaxNormThreads) rms_norm_grad_kernel(const NormGradParams p) {
+  __shared__ float buf[2][2 * kMaxNormWarps];
+  const int T = blockDim.x, warps = T >> 5;
+  Vec8 g[C], gg[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int v = threadIdx.x + c * T;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) g[c].v[i] = gg[c].v[i] = 0.0f;
+    if (v < p.nvec) g[c] = load_weight(p.g, p.g_f32, v);
+  }
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
+    const int64_t base = row * p.nvec;
+    Vec8 h[C], t[C];
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int v = threadIdx.x + c * T;
+      if (v < p.nvec) {
+        h[c] = load8<HT>(p.h, base + v);
+        t[c] = load8<GT>(p.gy, base + v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) h[c].v[i] = t[c].v[i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        s[0] = fmaf(h[c].v[i], h[c].v[i], s[0]);
+        s[1] = fmaf(t[c].v[i] * g[c].v[i], h[c].v[i], s[1]);
+      }
+    block_sums<2>(s, buf[flip], warps);
+    const float r = rsqrtf(fmaf(s[0], p.inv_d, p.eps));
+    const float k = r * r * r * (s[1] * p.inv_d);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int v = threadIdx.x + c * T;
+      if (v < p.nvec) {
+        Vec8 o;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          gg[c].v[i] = fmaf(t[c].v[i], h[c].v[i] * r, gg[c].v[i]);
+          o.v[i] = fmaf(t[c].v[i] * g[c].v[i], r, -h[c].v[i] * k);
+        }
+        if (p.gres) {
+          const Vec8 a = load8<HT>(p.gres, base + v);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) o.v[i] += a.v[i];
+        }
+        store8<HT>(p.gx, base + v, o);
+      }
+    }
+  }
+  if (p.part) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int v = threadIdx.x + c * T;
+      if (v < p.nvec) store8<float>(p.part, static_cast<int64_t>(blockIdx.x) * p.nvec + v, gg[c]);
+    }
+  }
+}
+
+// gg[c] = sum of the `rows` partial rows: a block per 32 columns, 32 rows at a time.
+__global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* part, int rows, int d, float* gg) {
+  __shared__ float buf[32][33];
+  pdl_wait();
+  const int col = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.0f;
+  if (col < d)
+#pragma unroll 4
+    for (int r = threadIdx.y; r < rows; r += 32) s += part[static_cast<int64_t>(r) * d + col];
+  buf[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && col < d) {
+    float t = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) t += buf[r][threadIdx.x];
+    gg[col] = t;
+  }
+}
+
+// Vecs per thread and threads per row.
+struct RowPlan {
+  int c, threads;
+};
+RowPlan row_plan(int nvec, int64_t N) {
+  RowPlan rp;
+  rp.c = nvec > 512 || (nvec > 64 && N > 1024) ? 2 : 1;
+  rp.threads = ((nvec + rp.c - 1) / rp.c + 31) / 32 * 32;
+  return rp;
+}
+
+constexpr int kNormBlocksPerSm = 12;
+constexpr int kNormGradBlocksPerSm = 6;
+
+unsigned row_grid(int64_t N, int threads, int per_sm) {
+  const int fit = 2048 / threads;
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * (fit < per_sm ? fit : per_sm);
+  return static_cast<unsigned>(N < cap ? N : cap);
+}
+
+template <typename XT, typename RT>
+void launch_norm_c(const NormParams& p, cudaStream_t s) {
+  const RowPlan rp = row_plan(p.nvec, p.N);
+  const unsigned grid = row_grid(p.N, rp.threads, kNormBlocksPerSm);
+  if (rp.c == 1) rms_norm_kernel<XT, RT, 1><<<grid, rp.threads, 0, s>>>(p);
+  else rms_norm_kernel<XT, RT, 2><<<grid, rp.threads, 0, s>>>(p);
+}
+
+template <typename XT>
+void launch_norm_x(const NormParams& p, int res_type, cudaStream_t s) {
+  if (!p.res) launch_norm_c<XT, NoRes>(p, s);
+  else if (res_type == KOLIBRI_TYPE_BF16) launch_norm_c<XT, __nv_bfloat16>(p, s);
+  else launch_norm_c<XT, float>(p, s);
+}
+
+template <typename GT, typename HT>
+void launch_norm_grad_c(const NormGradParams& p, const RowPlan& rp, unsigned grid, cudaStream_t s) {
+  if (rp.c == 1) rms_norm_grad_kernel<GT, HT, 1><<<grid, rp.threads, 0, s>>>(p);
+  else rms_norm_grad_kernel<GT, HT, 2><<<grid, rp.threads, 0, s>>>(p);
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const void* x, int x_type, const void* res, int res_type, const void* weight,
+                            int weight_type, float eps, int64_t N, int32_t d, void* res_out, void* y,
+                            void* y8, float* scales, cudaStream_t s) {
+  NormParams p{};
+  p.x = x;
+  p.res = res;
+  p.g = weight;
+  p.res_out = res_out;
+  p.y = y;
+  p.y8 = static_cast<uint8_t*>(y8);
+  p.scales = scales;
+  p.N = N;
+  p.nvec = d / kVec;
+  p.groups = (d + 127) / 128;
+  p.g_f32 = weight_type == KOLIBRI_TYPE_F32;
+  p.inv_d = 1.0f / static_cast<float>(d);
+  p.eps = eps;
+  if (x_type == KOLIBRI_TYPE_BF16) launch_norm_x<__nv_bfloat16>(p, res_type, s);
+  else launch_norm_x<float>(p, res_type, s);
+  return cudaGetLastError();
+}
+
+size_t rms_norm_grad_ws_bytes(int64_t N, int32_t d) {
+  const RowPlan rp = row_plan(d / kVec, N);
+  return sizeof(float) * static_cast<size_t>(row_grid(N, rp.threads, kNormGradBlocksPerSm)) * d;
+}
+
+cudaError_t launch_rms_norm_grad(const void* gy, int gy_type, const void* h, int h_type,
+                                 const void* weight, int weight_type, float eps, const void* gres,
+                                 int64_t N, int32_t d, void* gx, float* gweight, void* ws,
+                                 cudaStream_t s) {
+  NormGradParams p{};
+  p.gy = gy;
+  p.h = h;
+  p.g = weight;
+  p.gres = gres;
+  p.gx = gx;
+  p.part = gweight ? static_cast<float*>(ws) : nullptr;
+  p.N = N;
+  p.nvec = d / kVec;
+  p.g_f32 = weight_type == KOLIBRI_TYPE_F32;
+  p.inv_d = 1.0f / static_cast<float>(d);
+  p.eps = eps;
+  const RowPlan rp = row_plan(p.nvec, N);
+  const unsigned grid = row_grid(N, rp.threads, kNormGradBlocksPerSm);
+  if (gy_type == KOLIBRI_TYPE_BF16) {
+    if (h_type == KOLIBRI_TYPE_BF16) launch_norm_grad_c<__nv_bfloat16, __nv_bfloat16>(p, rp, grid, s);
+    else launch_norm_grad_c<__nv_bfloat16, float>(p, rp, grid, s);
+  } else {
+    if (h_type == KOLIBRI_TYPE_BF16) launch_norm_grad_c<float, __nv_bfloat16>(p, rp, grid, s);
+    else launch_norm_grad_c<float, float>(p, rp, grid, s);
+  }
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || !gweight) return err;
+  return launch_pdl(norm_weight_sum_kernel, dim3((d + 31) / 32), dim3(32, 32), 0, s, dim3(0, 0, 0),
+                    static_cast<const float*>(p.part), static_cast<int>(grid), static_cast<int>(d), gweight);
+}
+
+}  // namespace kolibri

@@ -75,6 +75,18 @@ enum {
     KOLIBRI_OP_EQB_BF16 = 3
 };
 
+/* Element type of an array that may hold either. */
+enum {
+    KOLIBRI_TYPE_BF16 = 0,
+    KOLIBRI_TYPE_F32 = 1
+};
+
+/* Score that kolibri_balance_loss normalises over the experts. */
+enum {
+    KOLIBRI_SCORE_SIGMOID = 0,   /* sigma(z), the router's gate */
+    KOLIBRI_SCORE_SOFTMAX = 1    /* exp(z) */
+};
+
 /* Limits.  E (experts) and K (top-K) must satisfy 1 <= K < E <= 512,
  * K <= 16, E % 4 == 0.  N (tokens) must satisfy 1 <= N and N*K < 2^31.
  * d (width) must satisfy 64 <= d, d % 64 == 0. */
@@ -511,6 +523,105 @@ KOLIBRI_API kolibri_status kolibri_expert_combine(const float *y_perm, const flo
                                                   const int32_t *inv, const float *gates,
                                                   int64_t N, int32_t d, int32_t K, float *y,
                                                   void *stream);
+
+/*
+ * The auxiliary balance loss over the router's scores, the per-expert counts
+ * and, if wanted, its gradient to the logits, in one pass over Z (the loss
+ * that "Kolibri Pre-Training from Scratch" 6.2 and 7 compare Exact Quantile
+ * Balancing with).  For each of S sequences, of T tokens each:
+ *   p_te = q_te / sum_j q_tj, q = sigma(z) or exp(z) as `score` says
+ *   c_e  = slots of the sequence routed to e,  f_e = E c_e / (K T)
+ *   P_e  = mean over its tokens of p_te,       loss = lambda sum_e f_e P_e
+ *   gz_te = grad_loss lambda / T p_te (f_e - sum_j f_j p_tj)
+ *           [ (1 - sigma(z_te)) with sigmoid scores ]
+ * (the counts carry no gradient).
+ *   z           [N, E] fp32 logits, finite or -infinity; a row whose logits are
+ *               all -infinity has p = 0 and gradient 0
+ *   ids         [N, K] int32 as kolibri_router_topk writes them.  An id outside
+ *               [0, E) is not counted and sets KOLIBRI_ERR_DEVICE in the device
+ *               status word; an id that stands twice in a row counts twice.
+ *   seq_offsets [S+1] int64: sequence s is rows [seq_offsets[s],
+ *               seq_offsets[s+1]); NULL: one sequence of all rows (S = 1).
+ *               Rows before the first and behind the last sequence (padding)
+ *               are not read.  A sequence without rows has loss 0, counts 0 and
+ *               P 0.  Offsets that decrease or leave [0, N] set
+ *               KOLIBRI_ERR_DEVICE; the outputs are then unspecified (no access
+ *               leaves the arrays).
+ *   score       KOLIBRI_SCORE_SIGMOID or KOLIBRI_SCORE_SOFTMAX
+ *   grad_loss   [S] fp32, dL_total/dloss_s, or NULL (ones); read only with gz
+ *   accumulate  0: gz is overwritten (padding rows with 0); 1: the gradient is
+ *               added to gz (padding rows are left as they were)
+ *   loss        [S] fp32, written;  counts [S, E] int32, written
+ *   prob        [S, E] fp32, written: P_e
+ *   gz          [N, E] fp32, or NULL: no gradient
+ *   ws          kolibri_balance_loss_workspace_size(N, E, S) bytes, 16-byte
+ *               aligned; need not be initialised
+ * K >= 1, K < E <= 512, E % 4 == 0, S E < 2^31.  Sums over tokens do not
+ * depend on the order in which blocks run: the same inputs give the same bits
+ * on the same GPU model.
+ */
+KOLIBRI_API size_t kolibri_balance_loss_workspace_size(int64_t N, int32_t E, int32_t S);
+KOLIBRI_API kolibri_status kolibri_balance_loss(const float *z, const int32_t *ids,
+                                                const int64_t *seq_offsets, int64_t N, int32_t E,
+                                                int32_t K, int32_t S, int32_t score, double lambda,
+                                                const float *grad_loss, int32_t accumulate,
+                                                float *loss, int32_t *counts, float *prob, float *gz,
+                                                void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The gradient of kolibri_balance_loss alone, for a backward pass that runs
+ * later: from the same z and seq_offsets and the counts [S, E] that call wrote.
+ * Arguments as there; gz is required.
+ */
+KOLIBRI_API kolibri_status kolibri_balance_loss_grad(const float *z, const int32_t *counts,
+                                                     const int64_t *seq_offsets, int64_t N,
+                                                     int32_t E, int32_t K, int32_t S, int32_t score,
+                                                     double lambda, const float *grad_loss,
+                                                     int32_t accumulate, float *gz, void *stream);
+
+/*
+ * Root-mean-square norm of the residual stream, the router's and the experts'
+ * input ("Kolibri 1 im Detail": bf16 tokens into the router, E4M3 activations
+ * with one fp32 scale per 1 x 128 group into the experts):
+ *   h = x + res (fp32), res_out = h rounded to res's type
+ *   y = h rsqrt(mean(h^2) + eps) weight, in fp32 from the unrounded h
+ * and from that y, each rounded once:
+ *   y    [N, d] bf16, or NULL
+ *   y8   [N, d] e4m3 with scales [N, ceil(d/128)] fp32, or both NULL: per group
+ *        of 128 columns (the last may be shorter) scale = max(amax |y|, 1e-30)
+ *        / 448 and y8 = e4m3(y / scale), so y is about y8 * scale
+ *   x, res  [N, d] of type x_type, res_type (KOLIBRI_TYPE_*); res may be NULL
+ *        (then res_out must be NULL)
+ *   weight  [d] of type weight_type;  res_out [N, d] of res_type, or NULL
+ * At least one of y and y8.  res_out may be res or x, and y may be x, where the
+ * types agree (in place); outputs must not overlap otherwise.
+ * d % 8 == 0, 8 <= d <= 16384, eps >= 0 (a row of zeros with eps = 0 is not a
+ * number).
+ */
+KOLIBRI_API kolibri_status kolibri_rms_norm(const void *x, int32_t x_type, const void *res,
+                                            int32_t res_type, const void *weight,
+                                            int32_t weight_type, float eps, int64_t N, int32_t d,
+                                            void *res_out, void *y, void *y8, float *scales,
+                                            void *stream);
+
+/*
+ * The gradient of kolibri_rms_norm.  The 8-bit output passes its gradient
+ * straight through: gy is the sum of what reaches y and y8.
+ *   gy [N, d] of gy_type: dL/dy;  h [N, d] of h_type: res_out (or x without res)
+ *   gres [N, d] of h_type, or NULL: dL/dres_out, added
+ *   gx [N, d] of h_type, written: dL/dh, the gradient of x and of res alike;
+ *        may be gres, h or (of the same type) gy
+ *   gweight [d] fp32, written if not NULL; ws then has
+ *        kolibri_rms_norm_grad_workspace_size(N, d) bytes, 16-byte aligned
+ *        (need not be initialised; may be NULL without gweight).
+ * Sums in fp32 in a fixed order.  Shapes as kolibri_rms_norm.
+ */
+KOLIBRI_API size_t kolibri_rms_norm_grad_workspace_size(int64_t N, int32_t d);
+KOLIBRI_API kolibri_status kolibri_rms_norm_grad(const void *gy, int32_t gy_type, const void *h,
+                                                 int32_t h_type, const void *weight,
+                                                 int32_t weight_type, float eps, const void *gres,
+                                                 int64_t N, int32_t d, void *gx, float *gweight,
+                                                 void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Diagnostic of the device-side failure path: launches one warp that waits,

@@ -1,0 +1,251 @@
+"""The balance loss, its counts and its gradient against the formulas in 64
+bits.
+
+Bars.  The fast exponential is within 2 + 1.2 |x| units of 2^-23 (CUDA's
+stated bound), 2^-18.5 for |x| <= 16; p = q / sum q carries it twice, with 25
+additions and two divisions of 2^-22: p is within 2^-17 relative, and so is P
+and 1 - sigma, plus (rows per warp) 2^-24 for P's sum: at most 64 rows here.
+With D = |f_e - 1| + sum_j |f_j - 1| p_j, the bracket f_e - sum f p is within
+2^-16 D, so gz within 2^-15 of scale p D slope.  L = lambda (1 + mean dot):
+within 2^-16 lambda (1 + mean_t sum_j |f_j - 1| p_j)."""
+import pytest
+import torch
+
+from expert_load_balancing_b200 import binding as B
+
+from gpu_helpers import check_status
+
+pytestmark = pytest.mark.gpu
+
+SCORES = [B.KOLIBRI_SCORE_SIGMOID, B.KOLIBRI_SCORE_SOFTMAX]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(kolibri_lib):
+    return kolibri_lib
+
+
+def _plain(z, ids, lam, cut, score, up):
+    """Loss, counts, P, gz and the bars of the last three, from the formulas."""
+    N, E = z.shape
+    K = ids.shape[1]
+    z = z.double()
+    out = dict(loss=[], counts=[], prob=[], gz=z.new_zeros(N, E), gbar=z.new_zeros(N, E), lbar=[])
+    for s in range(len(cut) - 1):
+        a, b = cut[s], cut[s + 1]
+        T = b - a
+        if T == 0:
+            out["loss"].append(z.new_zeros(()))
+            out["lbar"].append(z.new_zeros(()))
+            out["counts"].append(torch.zeros(E, dtype=torch.int64, device=z.device))
+            out["prob"].append(z.new_zeros(E))
+            continue
+        c = torch.zeros(E, dtype=torch.int64, device=z.device)
+        c.index_add_(0, ids[a:b].reshape(-1).long(), torch.ones(T * K, dtype=torch.int64, device=z.device))
+        f = c.double() * E / (K * T)
+        zz = z[a:b]
+        logq = zz if score == B.KOLIBRI_SCORE_SOFTMAX else torch.nn.functional.logsigmoid(zz)
+        none = (zz == -torch.inf).all(1, keepdim=True)
+        p = torch.softmax(torch.where(none, 0.0, logq), 1) * ~none
+        slope = torch.ones_like(p) if score == B.KOLIBRI_SCORE_SOFTMAX else torch.sigmoid(-zz)
+        k = lam * float(up[s]) / T
+        out["gz"][a:b] = k * p * (f - (p * f).sum(1, keepdim=True)) * slope
+        D = (f - 1).abs() + (p * (f - 1).abs()).sum(1, keepdim=True)
+        out["gbar"][a:b] = 2.0 ** -15 * abs(k) * p * D * slope + 1e-37
+        out["counts"].append(c)
+        out["prob"].append(p.mean(0))
+        out["loss"].append(lam * (f * out["prob"][-1]).sum())
+        out["lbar"].append(2.0 ** -16 * abs(lam) * (1 + (p * (f - 1).abs()).sum(1).mean()))
+    for n in ("loss", "counts", "prob", "lbar"):
+        out[n] = torch.stack(out[n])
+    return out
+
+
+def _check(got, want):
+    loss, counts, prob, gz = got
+    assert torch.equal(counts.long(), want["counts"])
+    assert ((loss.double() - want["loss"]).abs() <= want["lbar"] + 1e-30).all()
+    assert ((prob.double() - want["prob"]).abs() <= 2.0 ** -16 * want["prob"] + 1e-37).all()
+    if gz is not None:
+        err = (gz.double() - want["gz"]).abs()
+        assert torch.isfinite(gz).all()
+        assert (err <= want["gbar"]).all(), float((err / want["gbar"].clamp_min(1e-300)).max())
+
+
+def _inputs(N, E, K, cut, seed, spread=1.5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = torch.randn(N, E, generator=g, device="cuda") * spread + torch.randn(E, generator=g, device="cuda")
+    ids = torch.topk(z + 0.2 * torch.randn(E, generator=g, device="cuda"), K, dim=1).indices.to(torch.int32)
+    S = len(cut) - 1
+    up = torch.rand(S, generator=g, device="cuda") * 2 - 0.5
+    return z, ids, torch.tensor(cut, dtype=torch.int64, device="cuda"), up
+
+
+CASES = [
+    (1, 4, 1, [0, 1]), (1, 384, 6, [0, 1]), (2, 8, 3, [0, 1, 2]), (5, 132, 8, [0, 0, 5, 5]), (7, 128, 8, [0, 7]),
+    (256, 384, 6, [0, 256]), (257, 260, 2, [0, 100, 100, 257]), (1000, 512, 16, [0, 1, 2, 3, 500, 1000]),
+    (4096, 384, 6, [0, 4096]), (5003, 128, 8, [0, 17, 4000, 4000, 4001, 5003]), (700, 64, 1, list(range(0, 701))),
+    (6000, 12, 5, [0, 2999, 6000]), (40001, 256, 4, [0, 12345, 40001]),
+]
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("N,E,K,cut", CASES)
+def test_loss_counts_and_gradient(N, E, K, cut, score):
+    z, ids, seq, up = _inputs(N, E, K, cut, N + E)
+    want = _plain(z, ids, 1e-3, cut, score, up)
+    one = len(cut) == 2
+    got = B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq, score=score, grad_loss=up, want_gz=True)
+    _check(got, want)
+    # forward alone, the gradient alone, and again: the same bits
+    loss, counts, prob, none = B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=None if one else seq, score=score)
+    assert none is None and torch.equal(loss, got[0]) and torch.equal(counts, got[1]) and torch.equal(prob, got[2])
+    gz = B.kolibri_balance_loss_grad(z, counts, K, 1e-3, seq_offsets=seq, score=score, grad_loss=up)
+    _check((loss, counts, prob, gz), want)
+    assert torch.equal(gz, got[3])
+    # added to what is there: one fp32 addition more
+    base = torch.randn_like(z) * 1e-6
+    acc = base.clone()
+    B.kolibri_balance_loss_grad(z, counts, K, 1e-3, seq_offsets=seq, score=score, grad_loss=up, gz=acc, accumulate=True)
+    total = base.double() + want["gz"]
+    assert ((acc.double() - total).abs() <= want["gbar"] + 2.0 ** -23 * (base.double().abs() + total.abs())).all()
+    acc2 = base.clone()
+    B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq, score=score, grad_loss=up, gz=acc2, accumulate=True)
+    assert torch.equal(acc, acc2)
+    check_status()
+
+
+@pytest.mark.parametrize("score", SCORES)
+def test_padding_is_not_read(score):
+    """Rows before the first and behind the last sequence hold NaN logits and ids of nowhere."""
+    N, E, K, cut = 900, 384, 6, [37, 400, 400, 811]
+    z, ids, seq, up = _inputs(N, E, K, cut, 3)
+    want = _plain(z, ids, 0.5, cut, score, up)
+    outside = torch.ones(N, dtype=torch.bool, device="cuda")
+    outside[37:811] = False
+    z[outside] = float("nan")
+    ids[outside] = 1 << 30
+    got = B.kolibri_balance_loss(z, ids, 0.5, seq_offsets=seq, score=score, grad_loss=up, want_gz=True)
+    _check(got, want)
+    assert not got[3][outside].any()
+    kept = torch.full((N, E), 3.0, device="cuda")
+    B.kolibri_balance_loss_grad(z, got[1], K, 0.5, seq_offsets=seq, score=score, grad_loss=up, gz=kept, accumulate=True)
+    assert (kept[outside] == 3.0).all()
+    check_status()
+
+
+@pytest.mark.parametrize("score", SCORES)
+def test_extreme_logits(score):
+    """-infinity for some experts and for a whole row, rows far below zero, far above, the type's lowest value."""
+    N, E, K = 64, 128, 4
+    z, ids, seq, up = _inputs(N, E, K, [0, N], 5)
+    z[:, 5] = -torch.inf
+    z[3] = -torch.inf
+    z[7] -= 300.0
+    z[9] -= 3000.0
+    z[11] += 80.0
+    z[13, ::2] = torch.finfo(torch.float32).min
+    want = _plain(z, ids, 1.0, [0, N], score, up)
+    got = B.kolibri_balance_loss(z, ids, 1.0, seq_offsets=seq, score=score, grad_loss=up, want_gz=True)
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[2]).all() and torch.isfinite(got[3]).all()
+    assert not got[3][3].any() and not got[3][:, 5].any()
+    # logits of this size enter the exponential unreduced: their rows are held to the units it is then off by
+    big = torch.zeros(N, 1, dtype=torch.float64, device="cuda")
+    big[[7, 9, 11]] = 1.0
+    slack = want["gbar"] * (1 + 64 * big)
+    assert ((got[3].double() - want["gz"]).abs() <= slack).all()
+    assert ((got[2].double() - want["prob"]).abs() <= 2.0 ** -14 * want["prob"] + 1e-37).all()
+    check_status()
+
+
+def test_bad_ids_and_offsets_are_reported():
+    N, E, K = 300, 64, 4
+    z, ids, seq, up = _inputs(N, E, K, [0, 100, N], 6)
+    for bad in (-1, E, 1 << 30):
+        broken = ids.clone()
+        broken[17, 2] = bad
+        _, counts, _, _ = B.kolibri_balance_loss(z, broken, 1e-3, seq_offsets=seq)
+        assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE
+        assert int(counts.sum()) == N * K - 1          # the others are counted
+    twice = ids.clone()
+    twice[:, 1] = twice[:, 0]
+    _, counts, _, _ = B.kolibri_balance_loss(z, twice, 1e-3)
+    assert int(counts.sum()) == N * K
+    assert torch.equal(counts[0].long(), torch.bincount(twice.reshape(-1).long(), minlength=E))
+    for cut in ([0, 200, 100], [-5, 100, N], [0, 100, N + 1], [300, 0, 300]):
+        B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=torch.tensor(cut, device="cuda"), want_gz=True)
+        assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE
+    check_status()
+
+
+def test_even_loads_have_the_formulas_loss():
+    """Every expert equally loaded: f = 1, so L = lambda and the gradient vanishes, exactly."""
+    N, E, K = 512, 64, 2
+    z = torch.randn(N, E, device="cuda")
+    ids = (torch.arange(N * K, device="cuda") % E).view(N, K).to(torch.int32)
+    loss, counts, prob, gz = B.kolibri_balance_loss(z, ids, 0.25, want_gz=True)
+    assert (counts == N * K // E).all() and float(loss) == 0.25 and not gz.any()
+
+
+@pytest.mark.parametrize("score", SCORES)
+def test_gradient_against_differences(score):
+    """Central differences of the formula's loss in 64 bits along a direction, per sequence weighted by up."""
+    N, E, K, cut = 48, 20, 3, [0, 11, 48]
+    z, ids, seq, up = _inputs(N, E, K, cut, 12, spread=1.0)
+    gz = B.kolibri_balance_loss(z, ids, 0.7, seq_offsets=seq, score=score, grad_loss=up, want_gz=True)[3]
+    v = torch.randn(N, E, device="cuda").double()
+
+    def total(zz):
+        return float((_plain(zz, ids, 0.7, cut, score, up)["loss"] * up.double()).sum())
+
+    e = 1e-5
+    diff = (total(z.double() + e * v) - total(z.double() - e * v)) / (2 * e)
+    terms = gz.double() * v
+    assert abs(float(terms.sum()) - diff) <= 2.0 ** -14 * float(terms.abs().sum()) + 1e-8
+
+
+def test_refusals():
+    z, ids, seq, up = _inputs(16, 64, 4, [0, 4, 16], 2)
+    for kw in (dict(z=z.double()), dict(z=z.t()), dict(ids=ids.long()), dict(ids=ids[:3]), dict(seq_offsets=seq.int()),
+               dict(grad_loss=up[:1]), dict(gz=z[:4]), dict(loss=up[:1]), dict(counts=ids), dict(prob=z),
+               dict(accumulate=True, want_gz=True), dict(ids=ids.cpu())):
+        a = dict(z=z, ids=ids, seq_offsets=seq) | kw
+        zz, ii = a.pop("z"), a.pop("ids")
+        with pytest.raises(ValueError):
+            B.kolibri_balance_loss(zz, ii, 1e-3, **a)
+    with pytest.raises(B.KolibriError):
+        B.kolibri_balance_loss(z, ids, 1e-3, score=5)
+    with pytest.raises(B.KolibriError):
+        B.kolibri_balance_loss(z, ids, float("nan"))
+    with pytest.raises(B.KolibriError):
+        B.kolibri_balance_loss(z, ids, 1e-3, ws=torch.empty(64, device="cuda", dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        B.kolibri_balance_loss_grad(z, ids, 4, 1e-3)
+
+
+def test_other_stream_and_graph():
+    N, E, K, cut = 3001, 384, 6, [0, 1000, 3001]
+    z, ids, seq, up = _inputs(N, E, K, cut, 9)
+    want = B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq, grad_loss=up, want_gz=True)
+    out = [torch.empty_like(t) for t in want]
+    ws = torch.empty(B.load().kolibri_balance_loss_workspace_size(N, E, 2), device="cuda", dtype=torch.uint8)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+
+    def run(stream=None):
+        B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq, grad_loss=up, loss=out[0], counts=out[1], prob=out[2],
+                               gz=out[3], ws=ws, stream=stream)
+
+    run(stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for t in out:
+        t.fill_(0)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    check_status()

@@ -1,0 +1,272 @@
+"""The norm in front of the router and its gradient against the formulas in
+64 bits.
+
+Bars.  Half a rounding step is 2^-8 (bf16), 2^-24 (fp32), 2^-4 (e4m3, and
+2^-10 below its smallest normal number 2^-6).
+- h = x + res is one fp32 addition (2^-24), the sum of squares of d <= 16384
+  terms in fp32 is a chain of at most 16 + 5 + 32 additions, each 2^-24, all
+  terms positive; the square root halves it; r, the two products and the
+  reciprocal add under ten more roundings.  So y before its last rounding is
+  within 64 * 2^-24 = 2^-18 of the formula, relative.
+- gx = r t - h r^3 mean(t h): both parts carry that error relative to the sum
+  of their terms' magnitudes: 2^-17 (|r t| + |h| r^3 mean|t h|).
+- gweight sums N terms in fp32: (N + 64) 2^-24 + 2^-17 of the sum of magnitudes."""
+import math
+
+import pytest
+import torch
+
+from expert_load_balancing_b200 import binding as B
+
+from gpu_helpers import check_status
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+BF, FP = torch.bfloat16, torch.float32
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(kolibri_lib):
+    return kolibri_lib
+
+
+def _randn(g, *shape, dtype=FP, scale=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def _inputs(N, d, xt, rt, wt, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    wide = torch.exp(torch.randn(d, generator=g, device="cuda"))
+    x = _randn(g, N, d, dtype=xt)
+    res = None if rt is None else (_randn(g, N, d) * wide).to(rt)
+    w = (1.0 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(wt)
+    return x, res, w
+
+
+def _within(got, want, bound, what):
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got.float()).all(), what
+    worst = float((err / bound.clamp_min(1e-300)).max())
+    assert worst <= 1.0, (what, worst)
+
+
+def _check_forward(x, res, w, eps, out, y8=True):
+    res_out, y, q, s = out
+    N, d = x.shape
+    h = x.double() + (0 if res is None else res.double())
+    want = h / torch.sqrt((h * h).mean(1, keepdim=True) + eps) * w.double()
+    if res is not None:
+        _within(res_out, h, (HALF[res.dtype] + 2.0 ** -24) * h.abs() + 1e-38, "res_out")
+    if y is not None:
+        _within(y, want, (HALF[BF] + 2.0 ** -18) * want.abs() + 1e-38, "y")
+    if q is not None:
+        G = -(-d // 128)
+        pad = want.new_zeros(N, G * 128)
+        pad[:, :d] = want
+        amax = pad.abs().view(N, G, 128).amax(2).clamp_min(1e-30)
+        _within(s, amax / 448, 2.0 ** -17 * amax / 448, "scales")
+        sc = s.double().repeat_interleave(128, 1)[:, :d]
+        v = (want / sc).abs()
+        half = torch.maximum(2.0 ** -4 * v, torch.full_like(v, 2.0 ** -10)) * (1 + 2.0 ** -10) + 2.0 ** -16 * v
+        _within(q.double() * sc, want, half * sc, "y8")
+
+
+@pytest.mark.parametrize("N,d,xt,rt,wt", [
+    (1, 2560, BF, BF, BF), (1, 8, BF, None, BF), (3, 16, FP, BF, FP), (7, 128, BF, FP, BF),
+    (5, 136, BF, BF, FP), (33, 1000, FP, FP, BF), (257, 2048, BF, BF, BF), (1500, 2560, BF, BF, BF),
+    (2049, 2560, FP, BF, BF), (1200, 640, BF, None, BF), (64, 4104, BF, BF, BF), (9, 8200, FP, FP, FP),
+    (5, 16384, BF, BF, BF), (1100, 16384, BF, FP, FP), (20000, 512, BF, FP, BF), (40000, 64, FP, None, FP)])
+def test_forward(N, d, xt, rt, wt):
+    x, res, w = _inputs(N, d, xt, rt, wt, 11 + N + d)
+    keep = x.clone(), None if res is None else res.clone()
+    out = B.kolibri_rms_norm(x, w, EPS, res=res, want_fp8=True)
+    torch.cuda.synchronize()
+    assert torch.equal(x, keep[0]) and (res is None or torch.equal(res, keep[1]))
+    _check_forward(x, res, w, EPS, out)
+    # each output alone gives the same bits
+    a = B.kolibri_rms_norm(x, w, EPS, res=res, want_fp8=False)
+    assert torch.equal(a[1], out[1]) and a[2] is None and a[3] is None
+    b = B.kolibri_rms_norm(x, w, EPS, res=res, want_y=False, want_fp8=True)
+    assert b[1] is None and torch.equal(b[2].view(torch.uint8), out[2].view(torch.uint8)) and torch.equal(b[3], out[3])
+
+
+@pytest.mark.parametrize("scale", [1e-18, 1e-3, 1e3, 1e15])
+def test_forward_of_small_and_large_values(scale):
+    x, res, w = _inputs(37, 2560, FP, FP, BF, 5)
+    x, res = x * scale, res * scale
+    out = B.kolibri_rms_norm(x, w, 0.0, res=res, want_fp8=True)
+    _check_forward(x, res, w, 0.0, out)
+
+
+def test_zero_rows_and_zero_groups():
+    x = torch.zeros(5, 512, device="cuda")
+    x[1] = torch.randn(512, device="cuda")
+    x[1, 128:256] = 0.0
+    w = torch.ones(512, device="cuda", dtype=BF)
+    _, y, q, s = B.kolibri_rms_norm(x, w, EPS, want_fp8=True)
+    assert not y[0].any() and not y[2:].any() and not q.float()[0].any()
+    assert torch.isfinite(s).all() and (s > 0).all()
+    assert not (q.float() * s.repeat_interleave(128, 1))[1, 128:256].any()
+    _check_forward(x, None, w, EPS, (None, y, q, s))
+
+
+def test_residual_that_cancels():
+    x, _, w = _inputs(9, 2048, BF, None, BF, 3)
+    res = -x
+    res[:, ::7] += 1.0
+    out = B.kolibri_rms_norm(x, w, EPS, res=res.contiguous(), want_fp8=True)
+    _check_forward(x, res, w, EPS, out)
+
+
+@pytest.mark.parametrize("N", [1, 3000])
+def test_in_place(N):
+    x, res, w = _inputs(N, 2560, BF, BF, BF, 8)
+    want = B.kolibri_rms_norm(x, w, EPS, res=res, want_fp8=True)
+    r1 = res.clone()
+    got = B.kolibri_rms_norm(x, w, EPS, res=r1, res_out=r1, want_fp8=True)
+    assert got[0].data_ptr() == r1.data_ptr() and torch.equal(r1, want[0]) and torch.equal(got[1], want[1])
+    x1, x2 = x.clone(), x.clone()
+    B.kolibri_rms_norm(x1, w, EPS, res=res, res_out=x1)
+    assert torch.equal(x1, want[0])
+    B.kolibri_rms_norm(x2, w, EPS, res=res, y=x2)
+    assert torch.equal(x2, want[1])
+
+
+def test_rows_behind_the_outputs_stay():
+    x, res, w = _inputs(100, 640, BF, BF, BF, 4)
+    y = torch.full((103, 640), 7.0, device="cuda", dtype=BF)
+    s = torch.full((103, 5), 7.0, device="cuda")
+    B.kolibri_rms_norm(x, w, EPS, res=res, y=y[:100], y8=torch.empty(100, 640, device="cuda", dtype=torch.float8_e4m3fn),
+                       scales=s[:100])
+    assert (y[100:] == 7.0).all() and (s[100:] == 7.0).all()
+
+
+def test_refusals():
+    x, res, w = _inputs(8, 64, BF, BF, BF, 1)
+    bad = [dict(x=x.half()), dict(x=x[:, ::2]), dict(w=w[:32]), dict(w=w.double()), dict(res=res[:4]), dict(res=res.half()),
+           dict(res=None, res_out=res), dict(res_out=res.float()), dict(y=x.float()), dict(y8=torch.empty(8, 64, device="cuda")),
+           dict(scales=torch.empty(8, 2, device="cuda"), want_fp8=True), dict(w=w.cpu())]
+    for kw in bad:
+        a = dict(x=x, w=w, res=res) | kw
+        xx, ww = a.pop("x"), a.pop("w")
+        with pytest.raises(ValueError):
+            B.kolibri_rms_norm(xx, ww, EPS, **a)
+    for kw in (dict(d=12), dict(eps=-1.0), dict(none=True)):
+        d = kw.get("d", 64)
+        xx = torch.zeros(4, d, device="cuda", dtype=BF)
+        with pytest.raises(B.KolibriError):
+            B.kolibri_rms_norm(xx, torch.ones(d, device="cuda", dtype=BF), kw.get("eps", EPS), want_y="none" not in kw)
+    with pytest.raises(B.KolibriError):
+        B.kolibri_rms_norm(x[:0], w, EPS)
+
+
+# ---------------------------------------------------------------- gradient
+
+def _grad64(gy, h, w, eps, gres):
+    h, gy, w = h.double(), gy.double(), w.double()
+    d = h.shape[1]
+    r = 1.0 / torch.sqrt((h * h).mean(1, keepdim=True) + eps)
+    t = gy * w
+    gx = r * t - h * r ** 3 * (t * h).mean(1, keepdim=True)
+    mag = (r * t).abs() + h.abs() * r ** 3 * (t * h).abs().mean(1, keepdim=True)
+    if gres is not None:
+        gx = gx + gres.double()
+    return gx, mag, (gy * h * r).sum(0), (gy * h * r).abs().sum(0)
+
+
+def _check_grad(gy, h, w, eps, gres, gx, gg):
+    want, mag, wg, wmag = _grad64(gy, h, w, eps, gres)
+    _within(gx, want, HALF[h.dtype] * want.abs() + 2.0 ** -17 * mag + 2.0 ** -22 * want.abs() + 1e-38, "gx")
+    if gg is not None:
+        _within(gg, wg, ((h.shape[0] + 64) * 2.0 ** -24 + 2.0 ** -17) * wmag + 1e-38, "gweight")
+
+
+@pytest.mark.parametrize("N,d,ht,gt,wt,gres", [
+    (1, 2560, BF, BF, BF, True), (1, 8, FP, FP, FP, False), (3, 24, BF, FP, BF, True), (333, 2048, FP, FP, BF, False),
+    (1500, 2560, BF, BF, BF, True), (2049, 640, BF, FP, FP, False), (64, 4104, FP, BF, BF, True),
+    (7, 8200, BF, BF, BF, False), (1030, 16384, FP, FP, FP, True), (5, 16384, BF, FP, BF, True), (30000, 128, BF, BF, BF, False)])
+def test_gradient(N, d, ht, gt, wt, gres):
+    h, _, w = _inputs(N, d, ht, None, wt, 21 + N)
+    g = torch.Generator(device="cuda").manual_seed(N + d)
+    gy = _randn(g, N, d, dtype=gt, scale=0.01)
+    gr = _randn(g, N, d, dtype=ht, scale=0.02) if gres else None
+    gx, gg = B.kolibri_rms_norm_grad(gy, h, w, EPS, gres=gr)
+    _check_grad(gy, h, w, EPS, gr, gx, gg)
+    # the same bits again, without the weight's gradient, and in place over gres and h
+    gx2, gg2 = B.kolibri_rms_norm_grad(gy, h, w, EPS, gres=gr)
+    assert torch.equal(gx, gx2) and torch.equal(gg, gg2)
+    gx3, none = B.kolibri_rms_norm_grad(gy, h, w, EPS, gres=gr, want_gweight=False)
+    assert none is None and torch.equal(gx, gx3)
+    if gr is not None:
+        B.kolibri_rms_norm_grad(gy, h, w, EPS, gres=gr, gx=gr)
+        assert torch.equal(gr, gx)
+    h1 = h.clone()
+    B.kolibri_rms_norm_grad(gy, h1, w, EPS, gres=None, gx=h1)
+    assert torch.equal(h1, B.kolibri_rms_norm_grad(gy, h, w, EPS)[0])
+
+
+def test_gradient_against_differences():
+    """L = sum y c: <gx, v> and <gweight, u> against central differences of the formula in 64 bits."""
+    h, _, w = _inputs(6, 264, FP, None, FP, 2)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    c, v, u = _randn(g, 6, 264), _randn(g, 6, 264), _randn(g, 264)
+    gx, gg = B.kolibri_rms_norm_grad(c, h, w, EPS)
+
+    def loss(hh, ww):
+        return (hh / torch.sqrt((hh * hh).mean(1, keepdim=True) + EPS) * ww * c.double()).sum()
+
+    e = 1e-6
+    for got, a, b in ((gx, (e * v.double(), 0), v), (gg, (0, e * u.double()), u)):
+        plus = loss(h.double() + a[0], w.double() + a[1])
+        minus = loss(h.double() - a[0], w.double() - a[1])
+        diff = float((plus - minus) / (2 * e))
+        terms = (got.double() * b.double())
+        # differences: e^2 times a third derivative of order one, and 2^-52 |L| / e
+        assert abs(float(terms.sum()) - diff) <= 2.0 ** -16 * float(terms.abs().sum()) + 1e-5
+
+
+def test_gradient_refusals():
+    h, _, w = _inputs(8, 64, BF, None, BF, 1)
+    for kw in (dict(gy=h[:4]), dict(gres=h.float()), dict(gx=h.float()), dict(gweight=w), dict(w=w[:8]), dict(gy=h.half()),
+               dict(ws=torch.empty(1 << 20, device="cuda"))):
+        a = dict(gy=h, w=w) | kw
+        gy, ww = a.pop("gy"), a.pop("w")
+        with pytest.raises(ValueError):
+            B.kolibri_rms_norm_grad(gy, h, ww, EPS, **a)
+    with pytest.raises(B.KolibriError):
+        B.kolibri_rms_norm_grad(h, h, w, EPS, ws=torch.empty(16, device="cuda", dtype=torch.uint8))
+
+
+def test_other_stream_and_graph():
+    x, res, w = _inputs(700, 2560, BF, BF, BF, 6)
+    want = B.kolibri_rms_norm(x, w, EPS, res=res, want_fp8=True)
+    gwant = B.kolibri_rms_norm_grad(want[1], want[0], w, EPS)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    out = [torch.empty_like(t) for t in want]
+    gx, gg = torch.empty_like(want[0]), torch.empty(2560, device="cuda")
+    ws = torch.empty(B.load().kolibri_rms_norm_grad_workspace_size(700, 2560), device="cuda", dtype=torch.uint8)
+
+    def run(stream=None):
+        B.kolibri_rms_norm(x, w, EPS, res=res, res_out=out[0], y=out[1], y8=out[2], scales=out[3], stream=stream)
+        B.kolibri_rms_norm_grad(out[1], out[0], w, EPS, gx=gx, gweight=gg, ws=ws, stream=stream)
+
+    def same():
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(out, want))
+        assert torch.equal(gx, gwant[0]) and torch.equal(gg, gwant[1])
+
+    run(stream=st)
+    same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for t in out + [gx, gg]:
+        t.view(torch.uint8).fill_(0)
+    for _ in range(2):
+        graph.replay()
+    same()
+    check_status()

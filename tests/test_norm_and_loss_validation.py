@@ -1,0 +1,97 @@
+"""Host-side argument checks of the norm, its gradient and the balance loss
+(no device needed: each case fails before anything is enqueued), and of the
+Python calls' own checks."""
+import math
+
+import pytest
+import torch
+
+INVALID, SHAPE, SMALL = 1, 2, 3
+F = 0x10000        # a 16-byte aligned address that is never dereferenced
+ODD = 0x10004      # a misaligned one
+BF16, F32 = 0, 1
+
+
+@pytest.fixture(scope="module")
+def lib(kolibri_lib):
+    return kolibri_lib
+
+
+def test_rms_norm_checks(lib):
+    f = lib.kolibri_rms_norm
+    #        x  xt    res rt    w  wt    eps   N   d     res_out y  y8 scales stream
+    assert f(None, BF16, F, BF16, F, BF16, 1e-6, 16, 2560, F, F, None, None, None) == INVALID
+    assert f(ODD, BF16, F, BF16, F, BF16, 1e-6, 16, 2560, F, F, None, None, None) == INVALID
+    assert f(F, 2, F, BF16, F, BF16, 1e-6, 16, 2560, F, F, None, None, None) == INVALID          # type codes
+    assert f(F, BF16, F, -1, F, BF16, 1e-6, 16, 2560, F, F, None, None, None) == INVALID
+    assert f(F, BF16, F, BF16, F, 7, 1e-6, 16, 2560, F, F, None, None, None) == INVALID
+    assert f(F, BF16, None, BF16, F, BF16, 1e-6, 16, 2560, F, F, None, None, None) == INVALID    # res_out needs res
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, 16, 2560, F, None, None, None, None) == INVALID    # no output
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, 16, 2560, F, F, F, None, None) == INVALID          # y8 without scales
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, 16, 2560, F, F, None, F, None) == INVALID
+    assert f(F, BF16, F, BF16, F, BF16, -1.0, 16, 2560, F, F, None, None, None) == INVALID
+    assert f(F, BF16, F, BF16, F, BF16, math.nan, 16, 2560, F, F, None, None, None) == INVALID
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, 0, 2560, F, F, None, None, None) == INVALID
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, 16, 2564, F, F, None, None, None) == SHAPE         # d % 8
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, 16, 16392, F, F, None, None, None) == SHAPE        # d > 16384
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, 1 << 31, 2560, F, F, None, None, None) == SHAPE
+
+
+def test_rms_norm_grad_checks(lib):
+    need = lib.kolibri_rms_norm_grad_workspace_size(4096, 2560)
+    assert need >= 4 * 2560 and need % 4 == 0
+    assert lib.kolibri_rms_norm_grad_workspace_size(0, 2560) == 0
+    assert lib.kolibri_rms_norm_grad_workspace_size(16, 2561) == 0
+    f = lib.kolibri_rms_norm_grad
+    #        gy gyt   h  ht    w  wt    eps   gres N     d     gx gw ws ws_bytes stream
+    assert f(None, BF16, F, BF16, F, BF16, 1e-6, None, 4096, 2560, F, F, F, need, None) == INVALID
+    assert f(F, BF16, ODD, BF16, F, BF16, 1e-6, None, 4096, 2560, F, F, F, need, None) == INVALID
+    assert f(F, 3, F, BF16, F, BF16, 1e-6, None, 4096, 2560, F, F, F, need, None) == INVALID
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, ODD, 4096, 2560, F, F, F, need, None) == INVALID
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, None, 4096, 2560, None, F, F, need, None) == INVALID
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, None, 4096, 2560, F, F, None, need, None) == INVALID   # gweight needs ws
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, None, 4096, 2560, F, F, F, need - 1, None) == SMALL
+    assert f(F, BF16, F, BF16, F, BF16, 1e-6, None, 4096, 4, F, F, F, need, None) == SHAPE
+
+
+def test_balance_loss_checks(lib):
+    size = lib.kolibri_balance_loss_workspace_size
+    n, E, K, S = 4096, 384, 6, 5
+    need = size(n, E, S)
+    assert need >= 4 * E * (S + 1)
+    assert size(0, E, S) == 0 and size(n, 0, S) == 0 and size(n, 513, S) == 0 and size(n, E, 0) == 0
+    f = lib.kolibri_balance_loss
+    #        z  ids seq N  E  K  S  score lambda gl acc loss counts prob gz ws ws_bytes stream
+    assert f(None, F, F, n, E, K, S, 0, 1e-3, F, 0, F, F, F, F, F, need, None) == INVALID
+    assert f(F, ODD, F, n, E, K, S, 0, 1e-3, F, 0, F, F, F, F, F, need, None) == INVALID
+    assert f(F, F, None, n, E, K, S, 0, 1e-3, F, 0, F, F, F, F, F, need, None) == INVALID       # no offsets: one sequence
+    assert f(F, F, F, n, E, K, 0, 0, 1e-3, F, 0, F, F, F, F, F, need, None) == INVALID
+    assert f(F, F, F, n, E, K, S, 2, 1e-3, F, 0, F, F, F, F, F, need, None) == INVALID          # score
+    assert f(F, F, F, n, E, K, S, 0, math.inf, F, 0, F, F, F, F, F, need, None) == INVALID
+    assert f(F, F, F, n, E, K, S, 0, 1e-3, F, 2, F, F, F, F, F, need, None) == INVALID          # accumulate
+    assert f(F, F, F, n, E, K, S, 0, 1e-3, F, 0, F, F, None, F, F, need, None) == INVALID
+    assert f(F, F, F, n, E, K, S, 0, 1e-3, F, 0, F, F, F, F, None, need, None) == INVALID
+    assert f(F, F, F, n, E, K, S, 0, 1e-3, F, 0, F, F, F, F, F, need - 1, None) == SMALL
+    assert f(F, F, F, n, E, E, S, 0, 1e-3, F, 0, F, F, F, F, F, need, None) == INVALID          # K >= E
+    assert f(F, F, F, n, 386, K, S, 0, 1e-3, F, 0, F, F, F, F, F, need, None) == SHAPE          # E % 4
+    assert f(F, F, F, n, E, K, 1 << 24, 0, 1e-3, F, 0, F, F, F, F, F, need, None) == SHAPE      # S E
+    g = lib.kolibri_balance_loss_grad
+    #        z  counts seq N  E  K  S  score lambda gl acc gz stream
+    assert g(F, None, F, n, E, K, S, 0, 1e-3, F, 0, F, None) == INVALID
+    assert g(F, F, F, n, E, K, S, 0, 1e-3, F, 0, None, None) == INVALID
+    assert g(F, F, F, n, E, K, S, 0, 1e-3, ODD, 0, F, None) == INVALID
+    assert g(F, F, None, n, E, K, 2, 0, 1e-3, F, 0, F, None) == INVALID
+    assert g(F, F, F, 0, E, K, S, 0, 1e-3, F, 0, F, None) == INVALID
+
+
+def test_python_calls_refuse_cpu_tensors_and_wrong_types():
+    from expert_load_balancing_b200 import binding as B
+    x = torch.zeros(4, 64)
+    with pytest.raises((ValueError, RuntimeError)):
+        B.kolibri_rms_norm(x, torch.ones(64), 1e-6)
+    with pytest.raises((ValueError, RuntimeError)):
+        B.kolibri_rms_norm_grad(x, x, torch.ones(64), 1e-6)
+    with pytest.raises((ValueError, RuntimeError)):
+        B.kolibri_balance_loss(x, torch.zeros(4, 2, dtype=torch.int32), 1e-3)
+    with pytest.raises((ValueError, RuntimeError)):
+        B.kolibri_balance_loss_grad(x, torch.zeros(1, 64, dtype=torch.int32), 2, 1e-3)
