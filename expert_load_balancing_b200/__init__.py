@@ -9,6 +9,7 @@ inputs; ``build`` compiles the library in-tree.
 from . import binding  # noqa: F401  (loads the library lazily, on first call)
 from .binding import (  # noqa: F401
     KolibriError,
+    expert_ffn_fp8_workspace,
     expert_ffn_workspace,
     kolibri_balance_loss,
     kolibri_balance_loss_grad,
@@ -25,6 +26,7 @@ from .binding import (  # noqa: F401
     kolibri_expert_dispatch,
     kolibri_expert_down,
     kolibri_expert_ffn,
+    kolibri_expert_ffn_fp8,
     kolibri_expert_gate_up,
     kolibri_expert_permute,
     kolibri_expert_permute_noalloc,

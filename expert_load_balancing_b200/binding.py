@@ -87,6 +87,8 @@ SIGNATURES = {
     "kolibri_rms_norm_grad_workspace_size": (_SZ, [_I64, _I32]),
     "kolibri_rms_norm_grad": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _I32, ctypes.c_float, _P, _I64, _I32, _P, _P,
                                              _P, _SZ, _P]),
+    "kolibri_expert_ffn_fp8_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
+    "kolibri_expert_ffn_fp8": (ctypes.c_int, [_P] * 15 + [_I64, _I32, _I32, _I32, _I32, _P, _SZ, _P]),
     "kolibri_device_status": (ctypes.c_int, [_P]),
     "kolibri_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint64, _P]),
 }
@@ -821,3 +823,49 @@ def kolibri_balance_loss_grad(z: torch.Tensor, counts: torch.Tensor, K: int, lam
            load().kolibri_balance_loss_grad(_ptr(z), _ptr(counts), _ptr(seq_offsets), N, E, K, S, score, lam,
                                             _ptr(grad_loss), 1 if accumulate else 0, _ptr(gz), _stream(stream)))
     return gz
+
+
+# ---------------------------------------------------------------- the experts on 8-bit operands
+
+def expert_ffn_fp8_workspace(N: int, d: int, F: int, K: int, shared: bool, device=None) -> torch.Tensor:
+    """Device workspace for kolibri_expert_ffn_fp8."""
+    n = int(load().kolibri_expert_ffn_fp8_workspace_size(N, d, F, K, 1 if shared else 0))
+    return torch.empty((max(n, 1),), dtype=torch.uint8, device=device or "cuda")
+
+
+def kolibri_expert_ffn_fp8(x8: torch.Tensor, x_scale: torch.Tensor, perm: torch.Tensor, offsets: torch.Tensor,
+                           inv: torch.Tensor, gates: torch.Tensor, w_gate_up: torch.Tensor, s_gate_up: torch.Tensor,
+                           w_down: torch.Tensor, s_down: torch.Tensor, ws_gate_up: torch.Tensor | None = None,
+                           ss_gate_up: torch.Tensor | None = None, ws_down: torch.Tensor | None = None,
+                           ss_down: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                           ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The expert layer on float8_e4m3fn operands: x8 * x_scale per 128 columns, weights * scale per 128 x 128 block.
+
+    y [N, d] bf16 = shared expert + sum_k gates[t,k] expert_{ids[t,k]}(x_t) (SwiGLU experts)."""
+    N, d = x8.shape
+    K = gates.shape[1]
+    E, F2, _ = w_gate_up.shape
+    F = F2 // 2
+    dev = x8.device
+    _on_current(x8, "x8")
+    shared = ws_gate_up is not None
+    if any((t is not None) != shared for t in (ss_gate_up, ws_down, ss_down)):
+        raise ValueError("shared expert: ws_gate_up, ss_gate_up, ws_down and ss_down go together")
+    if y is None:
+        y = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+    if ws is None:
+        ws = expert_ffn_fp8_workspace(N, d, F, K, shared, dev)
+    f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+    _need_all(dev, (x8, f8, (N, d), "x8"), (x_scale, f32, (N, d // 128), "x_scale"), (perm, i32, (N * K,), "perm"),
+              (offsets, torch.int64, (E + 1,), "offsets"), (inv, i32, (N * K,), "inv"), (gates, f32, (N, K), "gates"),
+              (w_gate_up, f8, (E, 2 * F, d), "w_gate_up"), (s_gate_up, f32, (E, 2 * F // 128, d // 128), "s_gate_up"),
+              (w_down, f8, (E, d, F), "w_down"), (s_down, f32, (E, d // 128, F // 128), "s_down"),
+              (ws_gate_up, f8, (2 * F, d), "ws_gate_up"), (ss_gate_up, f32, (2 * F // 128, d // 128), "ss_gate_up"),
+              (ws_down, f8, (d, F), "ws_down"), (ss_down, f32, (d // 128, F // 128), "ss_down"),
+              (y, torch.bfloat16, (N, d), "y"), (ws, torch.uint8, (ws.numel(),), "ws"))
+    _check("kolibri_expert_ffn_fp8",
+           load().kolibri_expert_ffn_fp8(
+               _ptr(x8), _ptr(x_scale), _ptr(perm), _ptr(offsets), _ptr(inv), _ptr(gates), _ptr(w_gate_up),
+               _ptr(s_gate_up), _ptr(w_down), _ptr(s_down), _ptr(ws_gate_up), _ptr(ss_gate_up), _ptr(ws_down),
+               _ptr(ss_down), _ptr(y), N, d, F, E, K, _ptr(ws), ws.numel(), _stream(stream)))
+    return y

@@ -510,6 +510,38 @@ kolibri_status kolibri_rms_norm_grad(const void* gy, int32_t gy_type, const void
                                         ws, static_cast<cudaStream_t>(stream)));
 }
 
+size_t kolibri_expert_ffn_fp8_workspace_size(int64_t N, int32_t d, int32_t F, int32_t K, int32_t shared) {
+  if (N < 1 || K < 1 || K > KOLIBRI_MAX_TOPK || N * (K + 1) >= kExpertRowLimit || !expert_fp8_shape_supported(d, F, 1))
+    return 0;
+  return expert_fp8_ws_bytes(N, d, F, K, shared != 0);
+}
+
+kolibri_status kolibri_expert_ffn_fp8(const void* x8, const float* x_scale, const int32_t* perm,
+                                      const int64_t* offsets, const int32_t* inv, const float* gates,
+                                      const void* w_gate_up, const float* s_gate_up, const void* w_down,
+                                      const float* s_down, const void* ws_gate_up, const float* ss_gate_up,
+                                      const void* ws_down, const float* ss_down, void* y, int64_t N, int32_t d,
+                                      int32_t F, int32_t E, int32_t K, void* ws, size_t ws_bytes, void* stream) {
+  if (!x8 || !x_scale || !perm || !offsets || !inv || !gates || !w_gate_up || !s_gate_up || !w_down || !s_down || !y ||
+      !ws)
+    return KOLIBRI_ERR_INVALID_ARG;
+  const bool shared = ws_gate_up != nullptr;
+  if ((ss_gate_up != nullptr) != shared || (ws_down != nullptr) != shared || (ss_down != nullptr) != shared)
+    return KOLIBRI_ERR_INVALID_ARG;
+  for (const void* q : {x8, static_cast<const void*>(x_scale), static_cast<const void*>(perm),
+                        static_cast<const void*>(offsets), static_cast<const void*>(inv),
+                        static_cast<const void*>(gates), w_gate_up, static_cast<const void*>(s_gate_up), w_down,
+                        static_cast<const void*>(s_down), ws_gate_up, static_cast<const void*>(ss_gate_up), ws_down,
+                        static_cast<const void*>(ss_down), static_cast<const void*>(y), static_cast<const void*>(ws)})
+    if (!aligned16(q)) return KOLIBRI_ERR_INVALID_ARG;
+  if (N < 1 || K < 1 || K > KOLIBRI_MAX_TOPK || E < 1 || d < 1 || F < 1) return KOLIBRI_ERR_INVALID_ARG;
+  if (!expert_fp8_shape_supported(d, F, E) || N * (K + 1) >= kExpertRowLimit) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < expert_fp8_ws_bytes(N, d, F, K, shared)) return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
+  const ExpertFp8Args a{x8, x_scale, perm, offsets, inv, gates, w_gate_up, s_gate_up, w_down, s_down, ws_gate_up,
+                        ss_gate_up, ws_down, ss_down, y, N, d, F, E, K, ws};
+  return from_cuda(launch_expert_ffn_fp8(a, static_cast<cudaStream_t>(stream)));
+}
+
 kolibri_status kolibri_selftest_bounded_wait(uint64_t limit_ns, void* stream) {
   if (limit_ns < 1000ull || limit_ns > 1000000000ull) return KOLIBRI_ERR_INVALID_ARG;
   bounded_wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(limit_ns);
@@ -522,7 +554,8 @@ kolibri_status kolibri_device_status(void* stream) {
   const unsigned v = status_take_api() | status_take_eqb() | status_take_noalloc() |
                      status_take_permute() | status_take_route() | status_take_logits() |
                      status_take_forward() | status_take_balance() | status_take_small() |
-                     status_take_experts() | status_take_decode() | status_take_balance_loss();
+                     status_take_experts() | status_take_decode() | status_take_balance_loss() |
+                     status_take_expert_fp8();
   if (v & kStatusReadFailed) return KOLIBRI_ERR_CUDA;
   if (v & kStatusTimeout) return KOLIBRI_ERR_TIMEOUT;
   if (v & kStatusBadInput) return KOLIBRI_ERR_DEVICE;

@@ -181,6 +181,31 @@ cudaError_t launch_score_grad(const float* z, const float* gs, int64_t n, float*
 cudaError_t launch_intervention(const float* z, const int32_t* ids, int64_t N, int32_t E, int32_t K,
                                 unsigned long long* total, double* rate, cudaStream_t s);
 
+// expert_fp8.cu: the expert layer on 8-bit operands.
+struct ExpertFp8Args {
+  const void* x8;
+  const float* x_scale;
+  const int32_t* perm;
+  const int64_t* offsets;
+  const int32_t* inv;
+  const float* gates;
+  const void* w_gate_up;
+  const float* s_gate_up;
+  const void* w_down;
+  const float* s_down;
+  const void* ws_gate_up;   // the shared expert's four, or all null
+  const float* ss_gate_up;
+  const void* ws_down;
+  const float* ss_down;
+  void* y;
+  int64_t N;
+  int32_t d, F, E, K;
+  void* ws;
+};
+bool expert_fp8_shape_supported(int32_t d, int32_t F, int32_t E);
+size_t expert_fp8_ws_bytes(int64_t N, int32_t d, int32_t F, int32_t K, bool shared);
+cudaError_t launch_expert_ffn_fp8(const ExpertFp8Args& a, cudaStream_t s);
+
 // norm.cu: the norm in front of the router and its gradient.
 cudaError_t launch_rms_norm(const void* x, int x_type, const void* res, int res_type, const void* weight,
                             int weight_type, float eps, int64_t N, int32_t d, void* res_out, void* y,
@@ -238,5 +263,6 @@ unsigned status_take_small();
 unsigned status_take_experts();
 unsigned status_take_decode();
 unsigned status_take_balance_loss();
+unsigned status_take_expert_fp8();
 
 }  // namespace kolibri

@@ -624,6 +624,41 @@ KOLIBRI_API kolibri_status kolibri_rms_norm_grad(const void *gy, int32_t gy_type
                                                  void *ws, size_t ws_bytes, void *stream);
 
 /*
+ * The expert layer on 8-bit operands ("Kolibri 1 im Detail", FP8 section:
+ * weights in E4M3 with one fp32 scale per 128 x 128 block, activations with
+ * one per 1 x 128 group; the router stays bf16): kolibri_expert_ffn with
+ *   x8 [N, d] e4m3, x_scale [N, d/128] fp32: as kolibri_rms_norm writes them,
+ *       x = x8 * x_scale
+ *   perm, offsets, inv from kolibri_expert_permute, gates [N, K] fp32;
+ *       offsets must run from 0 to N K
+ *   w_gate_up [E, 2F, d] e4m3 (per expert the F gate rows, then the F up rows),
+ *       s_gate_up [E, 2F/128, d/128] fp32;  w_down [E, d, F] e4m3,
+ *       s_down [E, d/128, F/128] fp32
+ *   shared expert ws_gate_up [2F, d], ss_gate_up [2F/128, d/128], ws_down
+ *       [d, F], ss_down [d/128, F/128], or all four NULL
+ *   y [N, d] bf16, written
+ * Arithmetic: products of e4m3 values accumulated on the tensor cores over 128
+ * values of k, then scaled and summed in fp32.  h = SiLU(g) u in fp32 is held
+ * in e4m3 with a scale max(amax |h|, 1e-30) / 448 per 128 units; an expert's
+ * output is rounded once to bf16, multiplied by its gate and summed in fp32 in
+ * the order shared, k = 0 .. K-1, and rounded to bf16.  Serving only: there is
+ * no gradient.
+ * Shapes: d % 256 == 0, d <= 8192, F % 128 == 0, F <= 8192, E <= 512, K <= 16,
+ * N (K + 1) < 2^31 - 512.  ws: kolibri_expert_ffn_fp8_workspace_size bytes
+ * (about N (K + 1) (F + 2 d)), 16-byte aligned, need not be initialised.
+ * Entries of perm or inv outside [0, N K) and offsets that do not run from 0
+ * to N K without decreasing set KOLIBRI_ERR_DEVICE; y is then unspecified.
+ */
+KOLIBRI_API size_t kolibri_expert_ffn_fp8_workspace_size(int64_t N, int32_t d, int32_t F,
+                                                         int32_t K, int32_t shared);
+KOLIBRI_API kolibri_status kolibri_expert_ffn_fp8(
+    const void *x8, const float *x_scale, const int32_t *perm, const int64_t *offsets,
+    const int32_t *inv, const float *gates, const void *w_gate_up, const float *s_gate_up,
+    const void *w_down, const float *s_down, const void *ws_gate_up, const float *ss_gate_up,
+    const void *ws_down, const float *ss_down, void *y, int64_t N, int32_t d, int32_t F, int32_t E,
+    int32_t K, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * Diagnostic of the device-side failure path: launches one warp that waits,
  * through the same bounded wait the kernels use, on a shared-memory barrier
  * that nothing arrives at.  After about limit_ns nanoseconds (1e3 to 1e9,

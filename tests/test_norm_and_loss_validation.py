@@ -95,3 +95,26 @@ def test_python_calls_refuse_cpu_tensors_and_wrong_types():
         B.kolibri_balance_loss(x, torch.zeros(4, 2, dtype=torch.int32), 1e-3)
     with pytest.raises((ValueError, RuntimeError)):
         B.kolibri_balance_loss_grad(x, torch.zeros(1, 64, dtype=torch.int32), 2, 1e-3)
+
+
+def test_expert_fp8_checks(lib):
+    size = lib.kolibri_expert_ffn_fp8_workspace_size
+    n, d, Fh, E, K = 4096, 2560, 512, 384, 6
+    need = size(n, d, Fh, K, 1)
+    assert need >= n * (K + 1) * (Fh + 4 * Fh // 128 + 2 * d) and size(n, d, Fh, K, 0) < need
+    assert size(0, d, Fh, K, 1) == 0 and size(n, 384, Fh, K, 1) == 0 and size(n, d, 64, K, 1) == 0
+    assert size(n, d, Fh, 17, 1) == 0
+    f = lib.kolibri_expert_ffn_fp8
+
+    def call(skip=(), odd=(), n=n, d=d, Fh=Fh, E=E, K=K, ws_bytes=need):
+        # x8 xs perm offs inv gates wgu sgu wd sd wgu_s sgu_s wd_s sd_s y ... ws
+        ptr = [None if i in skip else ODD if i in odd else F for i in range(16)]
+        return f(*ptr[:15], n, d, Fh, E, K, ptr[15], ws_bytes, None)
+
+    for i in range(16):
+        assert call(skip=(i,)) == INVALID, i            # one of the shared four alone missing is refused too
+        assert call(odd=(i,)) == INVALID, i
+    assert call(ws_bytes=need - 1) == SMALL
+    assert call(n=0) == INVALID and call(K=0) == INVALID and call(K=17) == INVALID and call(E=0) == INVALID
+    assert call(d=2432) == SHAPE and call(Fh=192) == SHAPE and call(E=513) == SHAPE and call(d=8448) == SHAPE
+    assert call(n=1 << 29) == SHAPE
