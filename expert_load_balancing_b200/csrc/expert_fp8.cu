@@ -18,12 +18,18 @@
 // is one register, and the 1 x 128 group maximum of h is a maximum over the
 // thread's own values and its partner's.
 //
-// The token rows are gathered by the TMA unit (tile::gather4) straight from
-// x8, so there is no dispatch pass.  The shared expert is one more group of
-// the same launch.  o is kept in bf16 (one rounding of 2^-9 per expert output,
-// below the 2^-9 of y itself once summed): it is written and read once, N K d
-// values, and would otherwise be the largest traffic of the layer.
+// A first pass copies the token rows to their grouped places and lays their
+// scales out by k block.  Gathering in the kernel was slower: by the TMA
+// unit's row gather (four rows per instruction) the loads alone took 108 us
+// where tiled loads take 55 (2049 tokens, 128 experts), and by cp.async, whose
+// requests queue behind the bulk loads, the projection took 1615 us instead of
+// 514 (16384 tokens, 384 experts).  The shared expert is one more group of the
+// same launch.  o is kept in fp16 with a power of two per 1 x 128 group, which
+// costs one rounding of 2^-12 relative to the group's largest value: it is
+// written and read once, N K d values, and in fp32 would be the largest traffic
+// of the layer.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "launch.h"
@@ -44,21 +50,24 @@ constexpr uint32_t kABytes = kTokRows * kKBlock;            // 16 KB
 constexpr uint32_t kBBytes = kWRows * kKBlock;              // 32 KB
 constexpr uint32_t kF8Stage = kABytes + kBBytes;
 constexpr int kSumWarps = 8;
-constexpr int kF8Threads = 64 + 32 * kSumWarps;             // warp 0 TMA, warp 1 MMA, warps 2..9 sums
+constexpr int kF8Threads = 128 + 32 * kSumWarps;            // warp 0 TMA, warp 1 MMA, warps 2, 3 token rows, warps 4..11 sums
+// Register split: a launch of 384 threads has 168 each, 64,512 in all; the
+// first warpgroup keeps 56 and the two summing ones take 224 (128 sums and two
+// 32-column loads): 128 * 56 + 256 * 224 = 64,512.
+constexpr int kF8RegsLow = 56, kF8RegsSum = 224;
 constexpr int kF8Groups = KOLIBRI_MAX_EXPERTS + 1;          // the experts and the shared expert
 constexpr float kF8AmaxMin = 1e-30f;
 constexpr float kF8Max = 448.0f;
 
 struct Fp8Params {
   const int64_t* offsets;   // [E + 1]
-  const int32_t* perm;      // [N K]; gate/up only
-  const float* a_scale;     // gate/up: [N, k_blocks] by token; down: [rows, k_blocks] by grouped row
   const float* w_scale;     // [E, w_rows / 128, k_blocks]
   const float* ws_scale;    // the shared expert's, or null
-  void* out;                // gate/up: h8 [rows, F]; down: o [rows, d] bf16
-  float* out_scale;         // gate/up: hs [rows, F / 128]
+  void* out;                // gate/up: h8 [rows, F]; down: o [rows, d] fp16
+  float* out_scale;         // gate/up: hs [F / 128][ld]; down: [rows, d / 128]
   int64_t N, NK;
-  int K, E, shared;
+  int64_t ld;               // row length of the transposed scales
+  int E, shared;
   int k_blocks, n_tiles, ncols, w_rows;
 };
 
@@ -70,7 +79,23 @@ struct F8Bars {
   __device__ __forceinline__ uint32_t tempty(int a) const { return base + 8u * (2 * kF8Stages + 2 + a); }
   __device__ __forceinline__ uint32_t holder() const { return base + 8u * (2 * kF8Stages + 4); }
 };
-constexpr int kF8BarBytes = 8 * (2 * kF8Stages + 5);
+constexpr int kF8BarBytes = 8 * (2 * kF8Stages + 5) + 8;     // a multiple of 16
+// Output rows pass through shared memory, 64 bytes of 32 rows at a time per
+// summing warp, so that four lanes write 64 contiguous bytes of a row: with a
+// thread writing its own row 16 bytes at a time the stores of a down tile took
+// 2.5 us of its 7.  Rows 80 bytes apart meet no bank twice.
+constexpr int kOutPitch = 80;
+constexpr int kOutBytes = 32 * kOutPitch;
+// Row scales ride with the operands: the scales of a k block lie side by side
+// by row, and one TMA copy brings the tile's (132 from the 16-byte boundary at
+// or below its first row) into one of eight slots.  A slot is overwritten eight
+// blocks later, when the MMAs of block + 4 are done, which wait for the sums of
+// block + 2: no barrier of its own.  Loaded by the summing threads one block
+// ahead, these 4-byte loads waited behind the bulk loads' queue: 538 us
+// instead of the layer's 374 without sums (16384 tokens).
+constexpr int kScaleSlots = 8;
+constexpr uint32_t kScaleBox = 132;
+constexpr uint32_t kScaleSlotBytes = 640;
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar,
                                             uint64_t policy) {
@@ -81,15 +106,28 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// Four rows of the map (box one row high), c0 .. c0 + 127 of each, to 512 bytes at dst.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int c0, int4 rows, uint32_t bar,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar),
-      "l"(policy)
-      : "memory");
+// Completion of a 32-column load, tied to its registers.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// acc += (v0, v1) * (f, f), two fp32 multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(float2& acc, uint32_t v0, uint32_t v1, uint64_t ff) {
+  uint64_t a = *reinterpret_cast<uint64_t*>(&acc);
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(a) : "r"(v0), "r"(v1), "l"(ff));
+  acc = *reinterpret_cast<float2*>(&a);
+}
+__device__ __forceinline__ uint64_t twice(float f) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(f)));
+  return r;
 }
 
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -117,6 +155,23 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
+}
+
+// 64 bytes of each of the warp's 32 rows (lane l holds row l's) to dst + l *
+// pitch, l < rows, by way of the warp's shared-memory buffer.
+__device__ __forceinline__ void store_rows(uint8_t* buf, const uint4 (&v)[4], uint8_t* dst, int64_t pitch, int rows) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + lane * kOutPitch + 16 * i) = v[i];
+  __syncwarp();
+  const int l0 = lane >> 2, piece = (lane & 3) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int l = 8 * i + l0;
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + l * kOutPitch + piece);
+    if (l < rows) *reinterpret_cast<uint4*>(dst + l * pitch + piece) = w;
+  }
+  __syncwarp();
 }
 
 // All threads: mt[g] = token blocks of the groups before g (mt[G] all of
@@ -186,21 +241,11 @@ struct F8Tiles {
   }
 };
 
-// The token of grouped row `row`; N (out of range, read as zeros) for a bad entry.
-__device__ __forceinline__ int64_t token_of(const Fp8Params& p, int64_t row) {
-  if (row >= p.NK) return row - p.NK;
-  const int32_t j = __ldg(p.perm + row);
-  if (j < 0 || j >= p.NK) {
-    raise_status(kStatusBadInput);
-    return p.N;
-  }
-  return j / p.K;
-}
-
 template <bool kGateUp>
 __global__ void __launch_bounds__(kF8Threads, 1)
     expert_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ CUtensorMap tm_ws, const Fp8Params p) {
+                      const __grid_constant__ CUtensorMap tm_as, const __grid_constant__ CUtensorMap tm_ws,
+                      const __grid_constant__ CUtensorMap tm_sc, const Fp8Params p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ int32_t mt_s[kF8Groups + 1];
   __shared__ int64_t off_s[kF8Groups + 1];
@@ -208,7 +253,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   __shared__ float amax_s[2][kTokRows];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  const F8Bars bars{ring + kF8Stage * kF8Stages};
+  // ring, scale slots (a TMA copy lands on a multiple of 128 bytes), barriers, output rows
+  const uint32_t slots = ring + kF8Stage * kF8Stages;
+  static_assert(kScaleSlotBytes % 128 == 0 && (kF8Stage * kF8Stages) % 128 == 0, "alignment of a TMA copy's target");
+  const F8Bars bars{slots + kScaleSlotBytes * kScaleSlots};
   uint8_t* const holder_ptr = smem_raw + (bars.holder() - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.E + p.shared;
@@ -237,52 +285,44 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const F8Tiles tiles{mt_s, off_s, G, p.n_tiles};
   const int64_t total = static_cast<int64_t>(mt_s[G]) * p.n_tiles;
 
-  if (warp == 0) {
-    // TMA producer: lane l gathers rows 4l .. 4l + 3 of the tile (gate/up); lane 0 loads the weights
+  if (warp < 4) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RegsLow));
+   if (warp == 0) {
+    // TMA: the weights, the grouped rows (boxes of 32, only those that exist) and their scales
     const uint64_t pol_w = policy_evict_first();
     const uint64_t pol_a = policy_evict_last();
-    int stage = 0;
+    int stage = 0, slot = 0;
     uint32_t phase = 0;
-    bool ok = true;
+    bool ok = lane == 0;
     for (int64_t tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       int g, valid, n;
       int64_t row0;
       tiles.map(tile, g, row0, valid, n);
       const bool sh = g == p.E;
       const CUtensorMap* tw = sh ? &tm_ws : &tm_w;
+      const CUtensorMap* ta = kGateUp && sh ? &tm_as : &tm_a;
+      const int a0 = static_cast<int>(kGateUp && sh ? row0 - p.NK : row0);
       const int w0 = (sh ? 0 : g * p.w_rows) + n * (kGateUp ? 128 : 256);
       const int w1 = w0 + (kGateUp ? p.w_rows / 2 : 128);
-      int4 rows = make_int4(0, 0, 0, 0);
-      const bool mine = kGateUp ? 4 * lane < valid : (lane < 4 && 32 * lane < valid);
-      if (kGateUp && mine) {
-        int r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          r[i] = 4 * lane + i < valid ? static_cast<int>(token_of(p, row0 + 4 * lane + i)) : static_cast<int>(p.N);
-        rows = make_int4(r[0], r[1], r[2], r[3]);
-      }
-      const uint32_t bytes = kBBytes + (kGateUp ? 512u * ((valid + 3) / 4) : 4096u * ((valid + 31) / 32));
+      const int boxes = (valid + 31) / 32;
+      const int s0 = static_cast<int>(row0 & ~static_cast<int64_t>(3));
+      const uint32_t bytes = kBBytes + 4096u * boxes + kScaleBox * 4u;
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         if (!mbar_wait(bars.empty(stage), phase ^ 1u)) { ok = false; break; }
-        const uint32_t a_dst = ring + kF8Stage * stage, b_dst = a_dst + kABytes;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bars.full(stage), bytes);
-          tma_load_2d(b_dst, tw, kb * kKBlock, w0, bars.full(stage), pol_w);
-          tma_load_2d(b_dst + kBBytes / 2, tw, kb * kKBlock, w1, bars.full(stage), pol_w);
-        }
-        __syncwarp();
-        if (mine) {
-          if constexpr (kGateUp) tma_gather4(a_dst + 512u * lane, &tm_a, kb * kKBlock, rows, bars.full(stage), pol_a);
-          else tma_load_2d(a_dst + 4096u * lane, &tm_a, kb * kKBlock, static_cast<int>(row0) + 32 * lane, bars.full(stage), pol_a);
-        }
+        const uint32_t a_dst = ring + kF8Stage * stage, b_dst = a_dst + kABytes, bar = bars.full(stage);
+        mbar_arrive_expect_tx(bar, bytes);
+        tma_load_2d(b_dst, tw, kb * kKBlock, w0, bar, pol_w);
+        tma_load_2d(b_dst + kBBytes / 2, tw, kb * kKBlock, w1, bar, pol_w);
+        for (int i = 0; i < boxes; ++i) tma_load_2d(a_dst + 4096u * i, ta, kb * kKBlock, a0 + 32 * i, bar, pol_a);
+        tma_load_2d(slots + kScaleSlotBytes * slot, &tm_sc, s0, kb, bar, pol_a);
+        slot = (slot + 1) % kScaleSlots;
         if (++stage == kF8Stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
+   } else if (warp == 1 && lane == 0) {
       constexpr uint32_t idesc = make_idesc_e4m3(kTokRows, kWRows);
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
@@ -308,106 +348,139 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           }
         }
       }
-    }
+   }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8RegsSum));
     // sums: thread = token row (TMEM lane quarter warp % 4), half of the columns.
     // Gate/up: half h holds the gates and the ups of units 64 h .. 64 h + 63.
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int r = quarter * 32 + lane;
+    uint8_t* const out_s = smem_raw + (bars.base + kF8BarBytes - raw) + (warp - 4) * kOutBytes;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    int buf = 0;
+    const float* const slots_s = reinterpret_cast<const float*>(smem_raw + (slots - raw));
+    int buf = 0, slot = 0;
     uint32_t buf_phase = 0;
     bool ok = true;
+    // the weight scales of a tile: lane l holds those of k blocks l and 32 + l, fetched a tile ahead
+    const int wblocks = p.w_rows / 128;
+    float wn[4] = {0.f, 0.f, 0.f, 0.f};
+    auto fetch = [&](int64_t t) {
+      int g, valid, n;
+      int64_t row0;
+      tiles.map(t, g, row0, valid, n);
+      const float* w0 = (g == p.E ? p.ws_scale : p.w_scale + static_cast<int64_t>(g) * wblocks * p.k_blocks) +
+                        (kGateUp ? n : 2 * n + half) * p.k_blocks;
+      const float* w1 = w0 + (wblocks / 2) * p.k_blocks;
+      if (lane < p.k_blocks) {
+        wn[0] = __ldg(w0 + lane);
+        if (kGateUp) wn[1] = __ldg(w1 + lane);
+      }
+      if (lane + 32 < p.k_blocks) {
+        wn[2] = __ldg(w0 + lane + 32);
+        if (kGateUp) wn[3] = __ldg(w1 + lane + 32);
+      }
+    };
+    if (blockIdx.x < total) fetch(blockIdx.x);
     for (int64_t tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       int g, valid, n;
       int64_t row0;
       tiles.map(tile, g, row0, valid, n);
-      const bool sh = g == p.E;
       const bool live = r < valid, warp_live = quarter * 32 < valid;
       const int64_t row = row0 + r;
-      int64_t arow = row;
-      if (kGateUp && live) arow = token_of(p, row);
-      const bool have = live && (!kGateUp || arow < p.N);
-      const float* as = p.a_scale + arow * p.k_blocks;
-      const int wblocks = p.w_rows / 128;
-      const float* wbase = sh ? p.ws_scale : p.w_scale + static_cast<int64_t>(g) * wblocks * p.k_blocks;
-      const float* w0 = wbase + (kGateUp ? n : 2 * n + half) * p.k_blocks;
-      const float* w1 = kGateUp ? w0 + (wblocks / 2) * p.k_blocks : w0;
-      float acc[4][32];
+      const int srow = static_cast<int>(row0 & 3) + r;
+      const float wc[4] = {wn[0], wn[1], wn[2], wn[3]};
+      if (tile + gridDim.x < total) fetch(tile + gridDim.x);
+      float2 acc[4][16];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
-      float sa = have ? __ldg(as) : 0.0f, s0 = __ldg(w0), s1 = __ldg(w1);
+        for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
       for (int kb = 0; kb < p.k_blocks; ++kb) {
-        const float f0 = sa * s0, f1 = sa * s1;
-        if (kb + 1 < p.k_blocks) {
-          sa = have ? __ldg(as + kb + 1) : 0.0f;
-          s0 = __ldg(w0 + kb + 1);
-          s1 = __ldg(w1 + kb + 1);
-        }
+        const float s0 = __shfl_sync(0xffffffffu, kb < 32 ? wc[0] : wc[2], kb & 31);
+        const float s1 = kGateUp ? __shfl_sync(0xffffffffu, kb < 32 ? wc[1] : wc[3], kb & 31) : s0;
         if (!mbar_wait(bars.tfull(buf), buf_phase)) { ok = false; break; }
         tc_fence_after();
         if (warp_live) {
+          // the next 32 columns are on their way while these are added
           const uint32_t t0 = tmem_base + lane_off + 256u * buf + (kGateUp ? 64u : 128u) * half;
+          const float sa = slots_s[slot * (kScaleSlotBytes / 4) + srow];
+          const uint64_t f0 = twice(sa * s0), f1 = twice(sa * s1);
+          uint32_t v[2][32];
+          tmem_ld32(t0, v[0]);
+          tmem_wait_ld32(v[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(t0 + (kGateUp && c >= 2 ? 64u : 0u) + 32u * c, v);
-            tmem_wait_ld();
-            const float f = c < 2 ? f0 : f1;
+            if (c < 3) tmem_ld32(t0 + (kGateUp && c >= 1 ? 64u : 0u) + 32u * (c + 1), v[(c + 1) & 1]);
+            const uint64_t f = c < 2 ? f0 : f1;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c][i] = fmaf(__uint_as_float(v[i]), f, acc[c][i]);
+            for (int i = 0; i < 16; ++i) fma2(acc[c][i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
+            if (c < 3) tmem_wait_ld32(v[(c + 1) & 1]);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.tempty(buf));
+        slot = (slot + 1) % kScaleSlots;
         if (++buf == 2) {
           buf = 0;
           buf_phase ^= 1u;
         }
       }
       if (!ok) break;
+      const int out_rows = valid - quarter * 32;       // rows of this warp that exist (may be <= 0)
+      const int64_t wrow = row0 + quarter * 32;
       if constexpr (kGateUp) {
         float amax = 0.0f;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            acc[c][i] = silu_mul(acc[c][i], acc[c + 2][i]);
-            amax = fmaxf(amax, fabsf(acc[c][i]));
+          for (int i = 0; i < 16; ++i) {
+            acc[c][i].x = silu_mul(acc[c][i].x, acc[c + 2][i].x);
+            acc[c][i].y = silu_mul(acc[c][i].y, acc[c + 2][i].y);
+            amax = fmaxf(amax, fmaxf(fabsf(acc[c][i].x), fabsf(acc[c][i].y)));
           }
         amax_s[half][r] = amax;
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kSumWarps) : "memory");
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");      // the two halves of these rows
         amax = fmaxf(fmaxf(amax, amax_s[half ^ 1][r]), kF8AmaxMin);
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kSumWarps) : "memory");
-        if (live) {
-          const float q = __fdiv_rn(kF8Max, amax);
-          uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + row * p.ncols + n * 128 + half * 64);
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");      // the two halves of these rows
+        const float q = __fdiv_rn(kF8Max, amax);
+        uint4 o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2* a = &acc[j >> 1][(j & 1) * 8];
+          o[j] = make_uint4(pack_e4m3(a[0].x * q, a[0].y * q, a[1].x * q, a[1].y * q),
+                            pack_e4m3(a[2].x * q, a[2].y * q, a[3].x * q, a[3].y * q),
+                            pack_e4m3(a[4].x * q, a[4].y * q, a[5].x * q, a[5].y * q),
+                            pack_e4m3(a[6].x * q, a[6].y * q, a[7].x * q, a[7].y * q));
+        }
+        store_rows(out_s, o, static_cast<uint8_t*>(p.out) + wrow * p.ncols + n * 128 + half * 64, p.ncols, out_rows);
+        if (live && half == 0) p.out_scale[n * p.ld + row] = __fdiv_rn(amax, kF8Max);
+      } else {
+        // the thread's 128 columns in fp16, scaled by the power of two that puts their largest in [2^14, 2^15)
+        float amax = kF8AmaxMin;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fmaxf(fabsf(acc[c][i].x), fabsf(acc[c][i].y)));
+        const uint32_t top = __float_as_uint(amax) & 0x7f800000u;
+        const float q = __uint_as_float((268u << 23) - top);
+        uint8_t* dst = static_cast<uint8_t*>(p.out) + (wrow * p.ncols + n * 256 + half * 128) * 2;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint4 o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float* a = &acc[j >> 1][(j & 1) * 16];
-            o[j] = make_uint4(pack_e4m3(a[0] * q, a[1] * q, a[2] * q, a[3] * q),
-                              pack_e4m3(a[4] * q, a[5] * q, a[6] * q, a[7] * q),
-                              pack_e4m3(a[8] * q, a[9] * q, a[10] * q, a[11] * q),
-                              pack_e4m3(a[12] * q, a[13] * q, a[14] * q, a[15] * q));
-          }
-          if (half == 0) p.out_scale[row * p.n_tiles + n] = __fdiv_rn(amax, kF8Max);
-        }
-      } else if (live) {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ncols + n * 256 + half * 128);
+            uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float* a = &acc[j >> 2][(j & 3) * 8];
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(a[2 * i], a[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            for (int i = 0; i < 4; ++i) {
+              const __half2 b = __floats2half2_rn(acc[c][4 * j + i].x * q, acc[c][4 * j + i].y * q);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            o[j] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          o[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          store_rows(out_s, o, dst + 64 * c, 2 * p.ncols, out_rows);
         }
+        if (live) p.out_scale[row * (p.ncols / 128) + 2 * n + half] = __uint_as_float(top - (14u << 23));
       }
     }
   }
@@ -419,66 +492,144 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem_base) : "memory");
 }
 
-// y[t] = o[NK + t] (shared) + sum_k gates[t,k] o[inv[t K + k]], fp32
-// multiply-adds in the order shared, k ascending; eight columns per thread.
-constexpr int kMaxCombineK = 16;
-__global__ void __launch_bounds__(256) combine_fp8_kernel(const uint4* __restrict__ o, const int32_t* __restrict__ inv,
-                                                          const float* __restrict__ gates, int64_t N, int K, int64_t NK,
-                                                          int shared, int vecs, uint4* __restrict__ y) {
-  __shared__ int64_t slot[kMaxCombineK + 1];
-  __shared__ float gate[kMaxCombineK + 1];
+// x8 rows by grouped row and their scales transposed, a block per 32 grouped
+// rows: xp[p] = x8[perm[p] / K] for p < NK, and st[b][p] = xs[token of p][b] for
+// p < NK + N (the shared expert's rows are the tokens in order, read in place).
+// A bad entry of perm is reported and gives token 0.
+constexpr int kGatherRows = 32;
+__global__ void __launch_bounds__(256) gather_fp8_kernel(const uint4* __restrict__ x8, const float* __restrict__ xs,
+                                                         const int32_t* __restrict__ perm, int64_t NK, int64_t rows,
+                                                         int K, int vecs, int k_blocks, int64_t ld,
+                                                         uint4* __restrict__ xp, float* __restrict__ st) {
+  __shared__ int32_t tok[kGatherRows];
+  __shared__ float sc[64][kGatherRows + 1];
   pdl_wait();
-  for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
-    __syncthreads();
-    if (threadIdx.x < K) {
-      const int32_t q = __ldg(inv + t * K + threadIdx.x);
-      const bool ok = q >= 0 && q < NK;
-      if (!ok) raise_status(kStatusBadInput);
-      slot[threadIdx.x + shared] = ok ? q : -1;
-      gate[threadIdx.x + shared] = __ldg(gates + t * K + threadIdx.x);
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kGatherRows;
+  const int n = static_cast<int>(rows - p0 < kGatherRows ? rows - p0 : kGatherRows);
+  if (threadIdx.x < n) {
+    const int64_t q = p0 + threadIdx.x;
+    int64_t t = q - NK;
+    if (q < NK) {
+      const int32_t j = perm[q];
+      const bool bad = j < 0 || j >= NK;
+      if (bad) raise_status(kStatusBadInput);
+      t = bad ? 0 : j / K;
     }
-    if (shared && threadIdx.x == 0) {
-      slot[0] = NK + t;
-      gate[0] = 1.0f;
+    tok[threadIdx.x] = static_cast<int32_t>(t);
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < kGatherRows / 8; ++i) {
+    const int r = warp + 8 * i;
+    if (r >= n) break;
+    const int64_t t = tok[r];
+    if (p0 + r < NK) {
+      const uint4* src = x8 + t * vecs;
+      uint4* dst = xp + (p0 + r) * vecs;
+#pragma unroll 5
+      for (int c = lane; c < vecs; c += 32) dst[c] = __ldg(src + c);
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < vecs; c += blockDim.x) {
-      float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-      for (int k = 0; k < K + shared; ++k) {
-        if (slot[k] < 0) continue;
-        const float s = gate[k];
-        const uint4 v = __ldg(o + slot[k] * vecs + c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[2 * i] = __fmaf_rn(s, __uint_as_float(w[i] << 16), a[2 * i]);
-          a[2 * i + 1] = __fmaf_rn(s, __uint_as_float(w[i] & 0xffff0000u), a[2 * i + 1]);
-        }
+    for (int b = lane; b < k_blocks; b += 32) sc[b][r] = __ldg(xs + t * k_blocks + b);
+  }
+  __syncthreads();
+  for (int b = warp; b < k_blocks; b += 8)
+    if (lane < n) st[b * ld + p0 + lane] = sc[b][lane];
+}
+
+// y[t] = o[NK + t] (shared) + sum_k gates[t,k] o[inv[t K + k]], fp32
+// multiply-adds in the order shared, k ascending; a block per token, eight
+// columns per thread, all KS = K + shared rows loaded before the first is added.
+constexpr int kCombineThreads = 1024;    // d = 8192
+template <int KS>
+__global__ void __launch_bounds__(kCombineThreads) combine_fp8_kernel(const uint4* o, const float* os, const int32_t* inv,
+                                                                      const float* gates, int64_t N, int K, int64_t NK,
+                                                                      int vecs, uint4* y) {
+  __shared__ int64_t slot[KS];
+  __shared__ float gate[KS];
+  const int shared = KS - K;
+  pdl_wait();
+  const int64_t t = blockIdx.x;
+  if (threadIdx.x < KS) {
+    const int k = static_cast<int>(threadIdx.x) - shared;
+    int64_t q = NK + t;
+    float g = 1.0f;
+    if (k >= 0) {
+      q = __ldg(inv + t * K + k);
+      g = __ldg(gates + t * K + k);
+      if (q < 0 || q >= NK) {
+        raise_status(kStatusBadInput);
+        q = 0;
       }
-      uint32_t w[4];
+    }
+    slot[threadIdx.x] = q;
+    gate[threadIdx.x] = g;
+  }
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= vecs) return;
+  uint4 v[KS];
+  float s[KS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(a[2 * i], a[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      y[t * vecs + c] = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int k = 0; k < KS; ++k) {
+    v[k] = __ldg(o + slot[k] * vecs + c);
+    s[k] = __ldg(os + slot[k] * (vecs / 16) + c / 16);
+  }
+  float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    const float f = gate[k] * s[k];                // exact: s is a power of two
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      a[2 * i] = __fmaf_rn(f, h.x, a[2 * i]);
+      a[2 * i + 1] = __fmaf_rn(f, h.y, a[2 * i + 1]);
     }
   }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(a[2 * i], a[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  y[t * vecs + c] = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct CombineArgs {
+  const uint4* o;
+  const float* os;
+  const int32_t* inv;
+  const float* gates;
+  int64_t N;
+  int K, ks, vecs;
+  uint4* y;
+};
+template <int KS>
+cudaError_t launch_combine_fp8(const CombineArgs& a, cudaStream_t s) {
+  if (a.ks == KS)
+    return launch_pdl(combine_fp8_kernel<KS>, dim3(static_cast<unsigned>(a.N)), dim3((a.vecs + 31) / 32 * 32), 0, s,
+                      dim3(0, 0, 0), a.o, a.os, a.inv, a.gates, a.N, a.K, a.N * a.K, a.vecs, a.y);
+  if constexpr (KS < KOLIBRI_MAX_TOPK + 1) return launch_combine_fp8<KS + 1>(a, s);
+  return cudaErrorInvalidValue;
 }
 
 template <bool kGateUp>
-cudaError_t launch_fp8_gemm(const void* a, int64_t a_rows, const void* w, const void* w_shared, const Fp8Params& p,
-                            cudaStream_t s) {
+cudaError_t launch_fp8_gemm(const void* a, int64_t a_rows, const void* a_shared, int64_t as_rows, const void* w,
+                            const void* w_shared, const float* scales, const Fp8Params& p, cudaStream_t s) {
   const uint64_t kdim = static_cast<uint64_t>(p.k_blocks) * kKBlock;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  CUtensorMap tm_a, tm_w, tm_ws;
-  if (!encode_2d(&tm_a, u8, 1, a, kdim, static_cast<uint64_t>(a_rows), kKBlock, kGateUp ? 1 : 32) ||
+  CUtensorMap tm_a, tm_w, tm_as, tm_ws, tm_sc;
+  if (!encode_2d(&tm_a, u8, 1, a, kdim, static_cast<uint64_t>(a_rows), kKBlock, 32) ||
+      !encode_2d(&tm_as, u8, 1, a_shared, kdim, static_cast<uint64_t>(as_rows), kKBlock, 32) ||
       !encode_2d(&tm_w, u8, 1, w, kdim, static_cast<uint64_t>(p.E) * p.w_rows, kKBlock, 128) ||
-      !encode_2d(&tm_ws, u8, 1, w_shared ? w_shared : w, kdim, static_cast<uint64_t>(p.w_rows), kKBlock, 128))
+      !encode_2d(&tm_ws, u8, 1, w_shared ? w_shared : w, kdim, static_cast<uint64_t>(p.w_rows), kKBlock, 128) ||
+      !encode_2d(&tm_sc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, scales, static_cast<uint64_t>(p.ld),
+                 static_cast<uint64_t>(p.k_blocks), kScaleBox, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   auto kern = expert_fp8_kernel<kGateUp>;
-  const size_t smem = 1024 + static_cast<size_t>(kF8Stage) * kF8Stages + kF8BarBytes;
+  const size_t smem = 1024 + static_cast<size_t>(kF8Stage) * kF8Stages + kF8BarBytes + kSumWarps * kOutBytes +
+                      kScaleSlots * kScaleSlotBytes;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   // token blocks: at most one partial block per group that has rows
@@ -487,21 +638,29 @@ cudaError_t launch_fp8_gemm(const void* a, int64_t a_rows, const void* w, const 
   const int64_t tiles = (rows / kTokRows + partial + p.shared) * p.n_tiles;
   const int64_t sms = device_sm_count();
   return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kF8Threads), smem, s,
-                    dim3(0, 0, 0), tm_a, tm_w, tm_ws, p);
+                    dim3(0, 0, 0), tm_a, tm_w, tm_as, tm_ws, tm_sc, p);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
+// h8 first: the hidden units in e4m3, then their scales, transposed.
 struct Fp8Layout {
-  size_t off_h8, off_hs, off_o, total;
+  int64_t rows, ld;         // grouped rows; ld: a multiple of 4, at least a scale box
+  size_t off_h8, off_hs, off_x, off_xs, off_o, off_os, total;
 };
 Fp8Layout fp8_layout(int64_t N, int32_t d, int32_t F, int32_t K, bool shared) {
-  const size_t rows = static_cast<size_t>(N) * K + (shared ? N : 0);
   Fp8Layout L{};
+  L.rows = N * K + (shared ? N : 0);
+  L.ld = (L.rows + 3) / 4 * 4;
+  if (L.ld < static_cast<int64_t>(kScaleBox)) L.ld = kScaleBox;
+  const size_t rows = static_cast<size_t>(L.rows), ld = static_cast<size_t>(L.ld);
   L.off_h8 = 0;
   L.off_hs = up256(rows * F);
-  L.off_o = L.off_hs + up256(rows * (F / 128) * sizeof(float));
-  L.total = L.off_o + up256(rows * d * sizeof(uint16_t));
+  L.off_x = L.off_hs + up256(ld * (F / 128) * sizeof(float));
+  L.off_xs = L.off_x + up256(static_cast<size_t>(N) * K * d);
+  L.off_o = L.off_xs + up256(ld * (d / 128) * sizeof(float));
+  L.off_os = L.off_o + up256(rows * d * sizeof(uint16_t));
+  L.total = L.off_os + up256(rows * (d / 128) * sizeof(float));
   return L;
 }
 
@@ -521,16 +680,19 @@ cudaError_t launch_expert_ffn_fp8(const ExpertFp8Args& a, cudaStream_t s) {
   const bool shared = a.ws_gate_up != nullptr;
   const Fp8Layout L = fp8_layout(a.N, a.d, a.F, a.K, shared);
   char* base = static_cast<char*>(a.ws);
-  const int64_t NK = a.N * a.K, rows = NK + (shared ? a.N : 0);
+  const int64_t NK = a.N * a.K;
+  cudaError_t err = launch_pdl(
+      gather_fp8_kernel, dim3(static_cast<unsigned>((L.rows + kGatherRows - 1) / kGatherRows)), dim3(256), 0, s,
+      dim3(0, 0, 0), static_cast<const uint4*>(a.x8), a.x_scale, a.perm, NK, L.rows, a.K, a.d / 16, a.d / 128, L.ld,
+      reinterpret_cast<uint4*>(base + L.off_x), reinterpret_cast<float*>(base + L.off_xs));
+  if (err != cudaSuccess) return err;
   Fp8Params p{};
   p.offsets = a.offsets;
   p.N = a.N;
   p.NK = NK;
-  p.K = a.K;
+  p.ld = L.ld;
   p.E = a.E;
   p.shared = shared ? 1 : 0;
-  p.perm = a.perm;
-  p.a_scale = a.x_scale;
   p.w_scale = a.s_gate_up;
   p.ws_scale = a.ss_gate_up;
   p.out = base + L.off_h8;
@@ -539,23 +701,23 @@ cudaError_t launch_expert_ffn_fp8(const ExpertFp8Args& a, cudaStream_t s) {
   p.n_tiles = a.F / 128;
   p.ncols = a.F;
   p.w_rows = 2 * a.F;
-  cudaError_t err = launch_fp8_gemm<true>(a.x8, a.N, a.w_gate_up, a.ws_gate_up, p, s);
+  err = launch_fp8_gemm<true>(base + L.off_x, NK, a.x8, a.N, a.w_gate_up, a.ws_gate_up,
+                              reinterpret_cast<const float*>(base + L.off_xs), p, s);
   if (err != cudaSuccess) return err;
-  p.a_scale = reinterpret_cast<const float*>(base + L.off_hs);
   p.w_scale = a.s_down;
   p.ws_scale = a.ss_down;
   p.out = base + L.off_o;
-  p.out_scale = nullptr;
+  p.out_scale = reinterpret_cast<float*>(base + L.off_os);
   p.k_blocks = a.F / 128;
   p.n_tiles = a.d / 256;
   p.ncols = a.d;
   p.w_rows = a.d;
-  err = launch_fp8_gemm<false>(base + L.off_h8, rows, a.w_down, a.ws_down, p, s);
+  err = launch_fp8_gemm<false>(base + L.off_h8, L.rows, base + L.off_h8, L.rows, a.w_down, a.ws_down,
+                               reinterpret_cast<const float*>(base + L.off_hs), p, s);
   if (err != cudaSuccess) return err;
-  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 8;
-  return launch_pdl(combine_fp8_kernel, dim3(static_cast<unsigned>(a.N < cap ? a.N : cap)), dim3(256), 0, s,
-                    dim3(0, 0, 0), reinterpret_cast<const uint4*>(base + L.off_o), a.inv, a.gates, a.N, a.K, NK,
-                    shared ? 1 : 0, a.d / 8, static_cast<uint4*>(a.y));
+  const CombineArgs c{reinterpret_cast<const uint4*>(base + L.off_o), reinterpret_cast<const float*>(base + L.off_os),
+                      a.inv, a.gates, a.N, a.K, a.K + (shared ? 1 : 0), a.d / 8, static_cast<uint4*>(a.y)};
+  return launch_combine_fp8<1>(c, s);
 }
 
 KOLIBRI_DEFINE_STATUS_TAKE(status_take_expert_fp8)

@@ -1,7 +1,7 @@
 """The expert layer on 8-bit operands against the formulas in 64 bits, in two
 steps: the hidden units that the call leaves at the front of its workspace
-(h8 [rows, F] e4m3, then from the next multiple of 256 bytes hs [rows, F/128]
-fp32) against SiLU(g) u, and y against the down projection of those very h.
+(h8 [rows, F] e4m3, then from the next multiple of 256 bytes hs [F/128, ld]
+fp32, ld = rows rounded up to 4 and at least 132) against SiLU(g) u, and y against the down projection of those very h.
 
 Bars.  Half a rounding step is 2^-4 (e4m3; 2^-10 absolute below 2^-6) and 2^-8
 (bf16).  A sum of n fp32 products is within n 2^-24 of the sum of their
@@ -78,7 +78,8 @@ def _wide(w, s):
 def _hidden(ws, rows, F):
     h8 = ws[:rows * F].view(F8).view(rows, F)
     at = (rows * F + 255) // 256 * 256
-    return h8, ws[at:at + rows * (F // 128) * 4].view(torch.float32).view(rows, F // 128)
+    ld = max((rows + 3) // 4 * 4, 132)
+    return h8, ws[at:at + ld * (F // 128) * 4].view(torch.float32).view(F // 128, ld)[:, :rows].t()
 
 
 def _check(c, y, ws):
