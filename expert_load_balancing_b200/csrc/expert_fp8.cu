@@ -11,10 +11,11 @@
 //
 // The scales are arbitrary fp32 numbers per 128 values of k, so the tensor
 // cores' block scaling (powers of two per 32) does not apply: each 128-wide k
-// block is multiplied into its own TMEM buffer (kind::f8f6f4, four MMAs of K =
-// 32, M = 128 token rows, N = 256 weight rows) and eight warps add it, scaled,
-// to fp32 sums in registers while the next block is multiplied into the other
-// buffer.  Token rows are the M side: a thread then owns one row, whose scale
+// block is multiplied into its own TMEM buffer (kind::f8f6f4, MMAs of K = 32,
+// M = 128 token rows, N = 128 weight rows, two halves per tile) and eight warps
+// add it, scaled, to fp32 sums in registers while the next block is multiplied
+// into the other buffer.  Each half has four warps and barriers of its own, so
+// the two halves' TMEM reads, multiply-adds and waits overlap.  Token rows are the M side: a thread then owns one row, whose scale
 // is one register, and the 1 x 128 group maximum of h is a maximum over the
 // thread's own values and its partner's.
 //
@@ -50,7 +51,7 @@ constexpr uint32_t kABytes = kTokRows * kKBlock;            // 16 KB
 constexpr uint32_t kBBytes = kWRows * kKBlock;              // 32 KB
 constexpr uint32_t kF8Stage = kABytes + kBBytes;
 constexpr int kSumWarps = 8;
-constexpr int kF8Threads = 128 + 32 * kSumWarps;            // warp 0 TMA, warp 1 MMA, warps 2, 3 token rows, warps 4..11 sums
+constexpr int kF8Threads = 128 + 32 * kSumWarps;            // warp 0 TMA, warps 1, 2 MMA, warps 4..11 sums
 // Register split: a launch of 384 threads has 168 each, 64,512 in all; the
 // first warpgroup keeps 56 and the two summing ones take 224 (128 sums and two
 // 32-column loads): 128 * 56 + 256 * 224 = 64,512.
@@ -71,15 +72,17 @@ struct Fp8Params {
   int k_blocks, n_tiles, ncols, w_rows;
 };
 
+// full(s): operands of stage s are there.  done(s, h): the MMAs of half h on
+// stage s are complete; both together free the stage.  free(b,
+// h): the sums of half h have read its columns of TMEM buffer b.
 struct F8Bars {
   uint32_t base;
   __device__ __forceinline__ uint32_t full(int s) const { return base + 8u * s; }
-  __device__ __forceinline__ uint32_t empty(int s) const { return base + 8u * (kF8Stages + s); }
-  __device__ __forceinline__ uint32_t tfull(int a) const { return base + 8u * (2 * kF8Stages + a); }
-  __device__ __forceinline__ uint32_t tempty(int a) const { return base + 8u * (2 * kF8Stages + 2 + a); }
-  __device__ __forceinline__ uint32_t holder() const { return base + 8u * (2 * kF8Stages + 4); }
+  __device__ __forceinline__ uint32_t done(int s, int h) const { return base + 8u * (kF8Stages + 2 * s + h); }
+  __device__ __forceinline__ uint32_t free(int b, int h) const { return base + 8u * (3 * kF8Stages + 2 * b + h); }
+  __device__ __forceinline__ uint32_t holder() const { return base + 8u * (3 * kF8Stages + 4); }
 };
-constexpr int kF8BarBytes = 8 * (2 * kF8Stages + 5) + 8;     // a multiple of 16
+constexpr int kF8BarBytes = 8 * (3 * kF8Stages + 5) + 8;     // a multiple of 16
 // Output rows pass through shared memory, 64 bytes of 32 rows at a time per
 // summing warp, so that four lanes write 64 contiguous bytes of a row: with a
 // thread writing its own row 16 bytes at a time the stores of a down tile took
@@ -220,24 +223,44 @@ __device__ void f8_tile_prefix(const Fp8Params& p, int G, int32_t* mt, int64_t* 
   __syncthreads();
 }
 
-struct F8Tiles {
+// The tiles of a block, blockIdx.x, blockIdx.x + gridDim.x, ...: the group and
+// feature block follow by steps, without a division or a search per tile
+// (called by whole warps; 32 groups are looked at together).
+struct F8Walk {
   const int32_t* mt;
   const int64_t* off;
-  int G, n_tiles;
-  // tile -> group, first grouped row, rows of the tile that exist, feature block
-  __device__ __forceinline__ void map(int64_t tile, int& g, int64_t& row0, int& valid, int& n) const {
-    const int mb = static_cast<int>(tile / n_tiles);
-    n = static_cast<int>(tile - static_cast<int64_t>(mb) * n_tiles);
-    int lo = 0, hi = G - 1;                   // last g with mt[g] <= mb
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (mt[mid] <= mb) lo = mid;
-      else hi = mid - 1;
+  int G, n_tiles, dm, dn;
+  int m, n, g;              // token block, feature block, group
+  __device__ __forceinline__ F8Walk(const int32_t* mt_, const int64_t* off_, int G_, int n_tiles_)
+      : mt(mt_), off(off_), G(G_), n_tiles(n_tiles_), g(0) {
+    m = static_cast<int>(blockIdx.x) / n_tiles;
+    n = static_cast<int>(blockIdx.x) - m * n_tiles;
+    dm = static_cast<int>(gridDim.x) / n_tiles;
+    dn = static_cast<int>(gridDim.x) - dm * n_tiles;
+    seek();
+  }
+  __device__ __forceinline__ bool valid() const { return m < mt[G]; }
+  __device__ __forceinline__ void seek() {          // g: the last group with mt[g] <= m
+    while (true) {
+      const int j = g + 1 + static_cast<int>(threadIdx.x & 31);
+      const uint32_t le = __ballot_sync(0xffffffffu, j < G && mt[j] <= m);
+      g += __popc(le);
+      if (le != 0xffffffffu) break;
     }
-    g = lo;
-    row0 = off[g] + static_cast<int64_t>(mb - mt[g]) * kTokRows;
-    const int64_t left = off[g + 1] - row0;
-    valid = static_cast<int>(left < kTokRows ? left : kTokRows);
+  }
+  __device__ __forceinline__ void step() {
+    m += dm;
+    n += dn;
+    if (n >= n_tiles) {
+      n -= n_tiles;
+      ++m;
+    }
+    seek();
+  }
+  __device__ __forceinline__ int64_t row0() const { return off[g] + static_cast<int64_t>(m - mt[g]) * kTokRows; }
+  __device__ __forceinline__ int rows() const {     // rows of the tile that exist
+    const int64_t left = off[g + 1] - row0();
+    return static_cast<int>(left < kTokRows ? left : kTokRows);
   }
 };
 
@@ -264,12 +287,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kF8Stages; ++s) {
       mbar_init(bars.full(s), 1);
-      mbar_init(bars.empty(s), 1);
+      mbar_init(bars.done(s, 0), 1);
+      mbar_init(bars.done(s, 1), 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(bars.tfull(a), 1);
-      mbar_init(bars.tempty(a), kSumWarps);
-    }
+    for (int b = 0; b < 2; ++b)
+      for (int h = 0; h < 2; ++h) mbar_init(bars.free(b, h), kSumWarps / 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -282,8 +304,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(holder_ptr);
-  const F8Tiles tiles{mt_s, off_s, G, p.n_tiles};
-  const int64_t total = static_cast<int64_t>(mt_s[G]) * p.n_tiles;
 
   if (warp < 4) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RegsLow));
@@ -293,26 +313,27 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const uint64_t pol_a = policy_evict_last();
     int stage = 0, slot = 0;
     uint32_t phase = 0;
-    bool ok = lane == 0;
-    for (int64_t tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      int g, valid, n;
-      int64_t row0;
-      tiles.map(tile, g, row0, valid, n);
+    bool ok = true;
+    for (F8Walk walk(mt_s, off_s, G, p.n_tiles); walk.valid() && ok; walk.step()) {
+      const int g = walk.g, n = walk.n, valid = walk.rows();
+      const int64_t row0 = walk.row0();
       const bool sh = g == p.E;
       const CUtensorMap* tw = sh ? &tm_ws : &tm_w;
       const CUtensorMap* ta = kGateUp && sh ? &tm_as : &tm_a;
       const int a0 = static_cast<int>(kGateUp && sh ? row0 - p.NK : row0);
+      // 64 weight rows each: gates and ups of the first 64 units, then of the others; or 256 columns
       const int w0 = (sh ? 0 : g * p.w_rows) + n * (kGateUp ? 128 : 256);
-      const int w1 = w0 + (kGateUp ? p.w_rows / 2 : 128);
+      const int wrow[4] = {w0, w0 + (kGateUp ? p.w_rows / 2 : 64), w0 + (kGateUp ? 64 : 128),
+                           w0 + (kGateUp ? p.w_rows / 2 + 64 : 192)};
       const int boxes = (valid + 31) / 32;
       const int s0 = static_cast<int>(row0 & ~static_cast<int64_t>(3));
       const uint32_t bytes = kBBytes + 4096u * boxes + kScaleBox * 4u;
-      for (int kb = 0; kb < p.k_blocks; ++kb) {
-        if (!mbar_wait(bars.empty(stage), phase ^ 1u)) { ok = false; break; }
+      for (int kb = 0; kb < p.k_blocks && lane == 0; ++kb) {
+        if (!mbar_wait(bars.done(stage, 0), phase ^ 1u) || !mbar_wait(bars.done(stage, 1), phase ^ 1u)) { ok = false; break; }
         const uint32_t a_dst = ring + kF8Stage * stage, b_dst = a_dst + kABytes, bar = bars.full(stage);
         mbar_arrive_expect_tx(bar, bytes);
-        tma_load_2d(b_dst, tw, kb * kKBlock, w0, bar, pol_w);
-        tma_load_2d(b_dst + kBBytes / 2, tw, kb * kKBlock, w1, bar, pol_w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tma_load_2d(b_dst + kBBytes / 4 * i, tw, kb * kKBlock, wrow[i], bar, pol_w);
         for (int i = 0; i < boxes; ++i) tma_load_2d(a_dst + 4096u * i, ta, kb * kKBlock, a0 + 32 * i, bar, pol_a);
         tma_load_2d(slots + kScaleSlotBytes * slot, &tm_sc, s0, kb, bar, pol_a);
         slot = (slot + 1) % kScaleSlots;
@@ -321,31 +342,34 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           phase ^= 1u;
         }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-   } else if (warp == 1 && lane == 0) {
-      constexpr uint32_t idesc = make_idesc_e4m3(kTokRows, kWRows);
+   } else if (warp <= 2 && lane == 0) {
+      // MMAs: one thread per half, so that one's waits and commits run under the other's multiplications.  The
+      // uses of a (buffer, half) stay in one thread: its barrier is waited for by parity, one use ahead at most.
+      constexpr uint32_t idesc = make_idesc_e4m3(kTokRows, kWRows / 2);
+      const int h = warp - 1;
+      const int64_t total = static_cast<int64_t>(mt_s[G]) * p.n_tiles;
+      int64_t left = blockIdx.x < total ? ((total - 1 - blockIdx.x) / gridDim.x + 1) * p.k_blocks : 0;   // k blocks
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
-      bool ok = true;
-      for (int64_t tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          if (!mbar_wait(bars.tempty(buf), buf_phase ^ 1u) || !mbar_wait(bars.full(stage), phase)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t a_addr = ring + kF8Stage * stage;
-          const uint64_t a_desc = sw128_desc(a_addr), b_desc = sw128_desc(a_addr + kABytes);
+      for (; left > 0; --left) {
+        if (!mbar_wait(bars.full(stage), phase)) break;
+        const uint32_t a_addr = ring + kF8Stage * stage;
+        const uint64_t a_desc = sw128_desc(a_addr), b_desc = sw128_desc(a_addr + kABytes + kBBytes / 2 * h);
+        if (!mbar_wait(bars.free(buf, h), buf_phase ^ 1u)) break;
+        tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)       // 32 e4m3 along k = 32 bytes inside the swizzle row
-            tc_mma_f8(tmem_base + 256u * buf, a_desc + 2u * ks, b_desc + 2u * ks, idesc, ks > 0 ? 1u : 0u);
-          tc_commit(bars.empty(stage));
-          tc_commit(bars.tfull(buf));
-          if (++stage == kF8Stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (++buf == 2) {
-            buf = 0;
-            buf_phase ^= 1u;
-          }
+        for (int ks = 0; ks < 4; ++ks)           // 32 e4m3 along k = 32 bytes inside the swizzle row
+          tc_mma_f8(tmem_base + 256u * buf + 128u * h, a_desc + 2u * ks, b_desc + 2u * ks, idesc, ks > 0 ? 1u : 0u);
+        tc_commit(bars.done(stage, h));
+        if (++stage == kF8Stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++buf == 2) {
+          buf = 0;
+          buf_phase ^= 1u;
         }
       }
    }
@@ -358,16 +382,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     uint8_t* const out_s = smem_raw + (bars.base + kF8BarBytes - raw) + (warp - 4) * kOutBytes;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float* const slots_s = reinterpret_cast<const float*>(smem_raw + (slots - raw));
-    int buf = 0, slot = 0;
-    uint32_t buf_phase = 0;
+    int stage = 0, buf = 0, slot = 0;
+    uint32_t phase = 0;
     bool ok = true;
     // the weight scales of a tile: lane l holds those of k blocks l and 32 + l, fetched a tile ahead
     const int wblocks = p.w_rows / 128;
     float wn[4] = {0.f, 0.f, 0.f, 0.f};
-    auto fetch = [&](int64_t t) {
-      int g, valid, n;
-      int64_t row0;
-      tiles.map(t, g, row0, valid, n);
+    auto fetch = [&](int g, int n) {
       const float* w0 = (g == p.E ? p.ws_scale : p.w_scale + static_cast<int64_t>(g) * wblocks * p.k_blocks) +
                         (kGateUp ? n : 2 * n + half) * p.k_blocks;
       const float* w1 = w0 + (wblocks / 2) * p.k_blocks;
@@ -380,16 +401,17 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         if (kGateUp) wn[3] = __ldg(w1 + lane + 32);
       }
     };
-    if (blockIdx.x < total) fetch(blockIdx.x);
-    for (int64_t tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      int g, valid, n;
-      int64_t row0;
-      tiles.map(tile, g, row0, valid, n);
+    F8Walk walk(mt_s, off_s, G, p.n_tiles);
+    if (walk.valid()) fetch(walk.g, walk.n);
+    while (walk.valid() && ok) {
+      const int n = walk.n, valid = walk.rows();
+      const int64_t row0 = walk.row0();
       const bool live = r < valid, warp_live = quarter * 32 < valid;
       const int64_t row = row0 + r;
       const int srow = static_cast<int>(row0 & 3) + r;
       const float wc[4] = {wn[0], wn[1], wn[2], wn[3]};
-      if (tile + gridDim.x < total) fetch(tile + gridDim.x);
+      walk.step();
+      if (walk.valid()) fetch(walk.g, walk.n);
       float2 acc[4][16];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -398,11 +420,16 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         const float s0 = __shfl_sync(0xffffffffu, kb < 32 ? wc[0] : wc[2], kb & 31);
         const float s1 = kGateUp ? __shfl_sync(0xffffffffu, kb < 32 ? wc[1] : wc[3], kb & 31) : s0;
-        if (!mbar_wait(bars.tfull(buf), buf_phase)) { ok = false; break; }
+        if (!mbar_wait(bars.done(stage, half), phase)) { ok = false; break; }
         tc_fence_after();
+        auto release = [&]() {           // the buffer's columns of this warp are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.free(buf, half));
+        };
         if (warp_live) {
           // the next 32 columns are on their way while these are added
-          const uint32_t t0 = tmem_base + lane_off + 256u * buf + (kGateUp ? 64u : 128u) * half;
+          const uint32_t t0 = tmem_base + lane_off + 256u * buf + 128u * half;
           const float sa = slots_s[slot * (kScaleSlotBytes / 4) + srow];
           const uint64_t f0 = twice(sa * s0), f1 = twice(sa * s1);
           uint32_t v[2][32];
@@ -410,20 +437,21 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           tmem_wait_ld32(v[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (c < 3) tmem_ld32(t0 + (kGateUp && c >= 1 ? 64u : 0u) + 32u * (c + 1), v[(c + 1) & 1]);
+            if (c < 3) tmem_ld32(t0 + 32u * (c + 1), v[(c + 1) & 1]);
             const uint64_t f = c < 2 ? f0 : f1;
 #pragma unroll
             for (int i = 0; i < 16; ++i) fma2(acc[c][i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
             if (c < 3) tmem_wait_ld32(v[(c + 1) & 1]);
+            if (c == 2) release();
           }
+        } else {
+          release();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.tempty(buf));
         slot = (slot + 1) % kScaleSlots;
-        if (++buf == 2) {
-          buf = 0;
-          buf_phase ^= 1u;
+        buf ^= 1;
+        if (++stage == kF8Stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
       if (!ok) break;
@@ -622,8 +650,8 @@ cudaError_t launch_fp8_gemm(const void* a, int64_t a_rows, const void* a_shared,
   CUtensorMap tm_a, tm_w, tm_as, tm_ws, tm_sc;
   if (!encode_2d(&tm_a, u8, 1, a, kdim, static_cast<uint64_t>(a_rows), kKBlock, 32) ||
       !encode_2d(&tm_as, u8, 1, a_shared, kdim, static_cast<uint64_t>(as_rows), kKBlock, 32) ||
-      !encode_2d(&tm_w, u8, 1, w, kdim, static_cast<uint64_t>(p.E) * p.w_rows, kKBlock, 128) ||
-      !encode_2d(&tm_ws, u8, 1, w_shared ? w_shared : w, kdim, static_cast<uint64_t>(p.w_rows), kKBlock, 128) ||
+      !encode_2d(&tm_w, u8, 1, w, kdim, static_cast<uint64_t>(p.E) * p.w_rows, kKBlock, 64) ||
+      !encode_2d(&tm_ws, u8, 1, w_shared ? w_shared : w, kdim, static_cast<uint64_t>(p.w_rows), kKBlock, 64) ||
       !encode_2d(&tm_sc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, scales, static_cast<uint64_t>(p.ld),
                  static_cast<uint64_t>(p.k_blocks), kScaleBox, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
