@@ -11,11 +11,10 @@
 //
 // The scales are arbitrary fp32 numbers per 128 values of k, so the tensor
 // cores' block scaling (powers of two per 32) does not apply: each 128-wide k
-// block is multiplied into its own TMEM buffer (kind::f8f6f4, MMAs of K = 32,
-// M = 128 token rows, N = 128 weight rows, two halves per tile) and eight warps
-// add it, scaled, to fp32 sums in registers while the next block is multiplied
-// into the other buffer.  Each half has four warps and barriers of its own, so
-// the two halves' TMEM reads, multiply-adds and waits overlap.  Token rows are the M side: a thread then owns one row, whose scale
+// block is multiplied into its own TMEM buffer (kind::f8f6f4, four MMAs of K =
+// 32, M = 128 token rows, N = 256 weight rows) and eight warps add it, scaled,
+// to fp32 sums in registers while the next block is multiplied into the other
+// buffer.  Token rows are the M side: a thread then owns one row, whose scale
 // is one register, and the 1 x 128 group maximum of h is a maximum over the
 // thread's own values and its partner's.
 //
@@ -46,7 +45,7 @@ using namespace gemm;
 constexpr int kTokRows = 128;            // token rows of a tile: the MMA's M
 constexpr int kWRows = 256;              // weight rows of a tile: the MMA's N
 constexpr int kKBlock = 128;             // k values per scale: one 128-byte swizzle row
-constexpr int kF8Stages = 4;
+constexpr int kMaxF8Stages = 4;
 constexpr uint32_t kABytes = kTokRows * kKBlock;            // 16 KB
 constexpr uint32_t kBBytes = kWRows * kKBlock;              // 32 KB
 constexpr uint32_t kF8Stage = kABytes + kBBytes;
@@ -72,28 +71,35 @@ struct Fp8Params {
   int k_blocks, n_tiles, ncols, w_rows;
 };
 
-// full(s): operands of stage s are there.  done(s, h): the MMAs of half h on
-// stage s are complete; both together free the stage.  free(b,
-// h): the sums of half h have read its columns of TMEM buffer b.
+// full(s): the operands of stage s are there.  done(s): the MMAs on stage s are
+// complete, which frees the stage and hands the buffer to the sums.  free(b):
+// the sums have read TMEM buffer b.
 struct F8Bars {
   uint32_t base;
   __device__ __forceinline__ uint32_t full(int s) const { return base + 8u * s; }
-  __device__ __forceinline__ uint32_t done(int s, int h) const { return base + 8u * (kF8Stages + 2 * s + h); }
-  __device__ __forceinline__ uint32_t free(int b, int h) const { return base + 8u * (3 * kF8Stages + 2 * b + h); }
-  __device__ __forceinline__ uint32_t holder() const { return base + 8u * (3 * kF8Stages + 4); }
+  __device__ __forceinline__ uint32_t done(int s) const { return base + 8u * (kMaxF8Stages + s); }
+  __device__ __forceinline__ uint32_t free(int b) const { return base + 8u * (2 * kMaxF8Stages + b); }
+  __device__ __forceinline__ uint32_t holder() const { return base + 8u * (2 * kMaxF8Stages + 2); }
 };
-constexpr int kF8BarBytes = 8 * (3 * kF8Stages + 5) + 8;     // a multiple of 16
-// Output rows pass through shared memory, 64 bytes of 32 rows at a time per
-// summing warp, so that four lanes write 64 contiguous bytes of a row: with a
-// thread writing its own row 16 bytes at a time the stores of a down tile took
-// 2.5 us of its 7.  Rows 80 bytes apart meet no bank twice.
-constexpr int kOutPitch = 80;
-constexpr int kOutBytes = 32 * kOutPitch;
+constexpr int kF8BarBytes = (8 * (2 * kMaxF8Stages + 3) + 15) / 16 * 16;
+// Output rows pass through shared memory, 64 (gate/up) or 128 bytes (down) of 32
+// rows at a time per summing warp, so that neighbouring lanes write whole
+// lines (a store takes a cycle for each line that it touches): with a thread
+// writing its own row 16 bytes at a time the stores of a down tile took 2.5 us
+// of its 7.  The 16 bytes between rows keep both ways free of bank conflicts.
+// The down projection pays for the larger buffers with a stage, of which it
+// needs fewer (four k blocks a tile).
+template <bool kGateUp>
+struct F8Cfg {
+  static constexpr int kStages = kGateUp ? 4 : 3;
+  static constexpr int kOutPitch = kGateUp ? 80 : 144;
+  static constexpr int kOutBytes = 32 * kOutPitch;
+};
 // Row scales ride with the operands: the scales of a k block lie side by side
 // by row, and one TMA copy brings the tile's (132 from the 16-byte boundary at
 // or below its first row) into one of eight slots.  A slot is overwritten eight
-// blocks later, when the MMAs of block + 4 are done, which wait for the sums of
-// block + 2: no barrier of its own.  Loaded by the summing threads one block
+// blocks later, when the MMAs of block + 4 (or + 5) are done, which wait for the
+// sums of block + 2: no barrier of its own.  Loaded by the summing threads one block
 // ahead, these 4-byte loads waited behind the bulk loads' queue: 538 us
 // instead of the layer's 374 without sums (16384 tokens).
 constexpr int kScaleSlots = 8;
@@ -106,6 +112,19 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -133,19 +152,6 @@ __device__ __forceinline__ uint64_t twice(float f) {
   return r;
 }
 
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Instruction descriptor, kind::f8f6f4: D fp32, A and B E4M3, both K-major.
 constexpr uint32_t make_idesc_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
@@ -160,17 +166,19 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return lo | (hi << 16);
 }
 
-// 64 bytes of each of the warp's 32 rows (lane l holds row l's) to dst + l *
+// 16 V bytes of each of the warp's 32 rows (lane l holds row l's) to dst + l *
 // pitch, l < rows, by way of the warp's shared-memory buffer.
-__device__ __forceinline__ void store_rows(uint8_t* buf, const uint4 (&v)[4], uint8_t* dst, int64_t pitch, int rows) {
+template <int V, int kOutPitch>
+__device__ __forceinline__ void store_rows(uint8_t* buf, const uint4 (&v)[V], uint8_t* dst, int64_t pitch, int rows) {
+  static_assert(V == 4 || V == 8, "lanes per row");
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + lane * kOutPitch + 16 * i) = v[i];
+  for (int i = 0; i < V; ++i) *reinterpret_cast<uint4*>(buf + lane * kOutPitch + 16 * i) = v[i];
   __syncwarp();
-  const int l0 = lane >> 2, piece = (lane & 3) * 16;
+  const int l0 = lane / V, piece = (lane % V) * 16;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int l = 8 * i + l0;
+  for (int i = 0; i < V; ++i) {
+    const int l = 32 / V * i + l0;
     const uint4 w = *reinterpret_cast<const uint4*>(buf + l * kOutPitch + piece);
     if (l < rows) *reinterpret_cast<uint4*>(dst + l * pitch + piece) = w;
   }
@@ -233,10 +241,11 @@ struct F8Walk {
   int m, n, g;              // token block, feature block, group
   __device__ __forceinline__ F8Walk(const int32_t* mt_, const int64_t* off_, int G_, int n_tiles_)
       : mt(mt_), off(off_), G(G_), n_tiles(n_tiles_), g(0) {
-    m = static_cast<int>(blockIdx.x) / n_tiles;
-    n = static_cast<int>(blockIdx.x) - m * n_tiles;
-    dm = static_cast<int>(gridDim.x) / n_tiles;
-    dn = static_cast<int>(gridDim.x) - dm * n_tiles;
+    const int first = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
+    m = first / n_tiles;
+    n = first - m * n_tiles;
+    dm = stride / n_tiles;
+    dn = stride - dm * n_tiles;
     seek();
   }
   __device__ __forceinline__ bool valid() const { return m < mt[G]; }
@@ -274,24 +283,23 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   __shared__ int64_t off_s[kF8Groups + 1];
   __shared__ int32_t warp_tot[kF8Threads / 32];
   __shared__ float amax_s[2][kTokRows];
+  using C = F8Cfg<kGateUp>;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
   // ring, scale slots (a TMA copy lands on a multiple of 128 bytes), barriers, output rows
-  const uint32_t slots = ring + kF8Stage * kF8Stages;
-  static_assert(kScaleSlotBytes % 128 == 0 && (kF8Stage * kF8Stages) % 128 == 0, "alignment of a TMA copy's target");
+  const uint32_t slots = ring + kF8Stage * C::kStages;
+  static_assert(kScaleSlotBytes % 128 == 0 && (kF8Stage * C::kStages) % 128 == 0, "alignment of a TMA copy's target");
   const F8Bars bars{slots + kScaleSlotBytes * kScaleSlots};
   uint8_t* const holder_ptr = smem_raw + (bars.holder() - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.E + p.shared;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kF8Stages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bars.full(s), 1);
-      mbar_init(bars.done(s, 0), 1);
-      mbar_init(bars.done(s, 1), 1);
+      mbar_init(bars.done(s), 1);
     }
-    for (int b = 0; b < 2; ++b)
-      for (int h = 0; h < 2; ++h) mbar_init(bars.free(b, h), kSumWarps / 2);
+    for (int b = 0; b < 2; ++b) mbar_init(bars.free(b), kSumWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -315,29 +323,28 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (F8Walk walk(mt_s, off_s, G, p.n_tiles); walk.valid() && ok; walk.step()) {
-      const int g = walk.g, n = walk.n, valid = walk.rows();
+      const int g = walk.g, n = walk.n;
       const int64_t row0 = walk.row0();
       const bool sh = g == p.E;
       const CUtensorMap* tw = sh ? &tm_ws : &tm_w;
       const CUtensorMap* ta = kGateUp && sh ? &tm_as : &tm_a;
       const int a0 = static_cast<int>(kGateUp && sh ? row0 - p.NK : row0);
-      // 64 weight rows each: gates and ups of the first 64 units, then of the others; or 256 columns
+      // the gate rows of 128 units and their up rows, or 256 columns
       const int w0 = (sh ? 0 : g * p.w_rows) + n * (kGateUp ? 128 : 256);
-      const int wrow[4] = {w0, w0 + (kGateUp ? p.w_rows / 2 : 64), w0 + (kGateUp ? 64 : 128),
-                           w0 + (kGateUp ? p.w_rows / 2 + 64 : 192)};
-      const int boxes = (valid + 31) / 32;
+      const int w1 = w0 + (kGateUp ? p.w_rows / 2 : 128);
+      const int boxes = (walk.rows() + 31) / 32;
       const int s0 = static_cast<int>(row0 & ~static_cast<int64_t>(3));
       const uint32_t bytes = kBBytes + 4096u * boxes + kScaleBox * 4u;
       for (int kb = 0; kb < p.k_blocks && lane == 0; ++kb) {
-        if (!mbar_wait(bars.done(stage, 0), phase ^ 1u) || !mbar_wait(bars.done(stage, 1), phase ^ 1u)) { ok = false; break; }
+        if (!mbar_wait(bars.done(stage), phase ^ 1u)) { ok = false; break; }
         const uint32_t a_dst = ring + kF8Stage * stage, b_dst = a_dst + kABytes, bar = bars.full(stage);
         mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tma_load_2d(b_dst + kBBytes / 4 * i, tw, kb * kKBlock, wrow[i], bar, pol_w);
+        tma_load_2d(b_dst, tw, kb * kKBlock, w0, bar, pol_w);
+        tma_load_2d(b_dst + kBBytes / 2, tw, kb * kKBlock, w1, bar, pol_w);
         for (int i = 0; i < boxes; ++i) tma_load_2d(a_dst + 4096u * i, ta, kb * kKBlock, a0 + 32 * i, bar, pol_a);
         tma_load_2d(slots + kScaleSlotBytes * slot, &tm_sc, s0, kb, bar, pol_a);
         slot = (slot + 1) % kScaleSlots;
-        if (++stage == kF8Stages) {
+        if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -345,42 +352,42 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
    } else if (warp <= 2 && lane == 0) {
-      // MMAs: one thread per half, so that one's waits and commits run under the other's multiplications.  The
-      // uses of a (buffer, half) stay in one thread: its barrier is waited for by parity, one use ahead at most.
-      constexpr uint32_t idesc = make_idesc_e4m3(kTokRows, kWRows / 2);
-      const int h = warp - 1;
+      // MMAs: one thread per TMEM buffer, so that one's waits and commits run under the other's
+      // multiplications (the queue behind a thread is too short for that).  The uses of a buffer stay in one
+      // thread: its barrier is waited for by parity, one use ahead at most.
+      constexpr uint32_t idesc = make_idesc_e4m3(kTokRows, kWRows);
+      const int buf = warp - 1;
       const int64_t total = static_cast<int64_t>(mt_s[G]) * p.n_tiles;
-      int64_t left = blockIdx.x < total ? ((total - 1 - blockIdx.x) / gridDim.x + 1) * p.k_blocks : 0;   // k blocks
-      int stage = 0, buf = 0;
+      const int64_t first = blockIdx.x, stride = gridDim.x;
+      const int64_t blocks = first < total ? ((total - 1 - first) / stride + 1) * p.k_blocks : 0;   // k blocks
+      int stage = buf;
       uint32_t phase = 0, buf_phase = 0;
-      for (; left > 0; --left) {
+      for (int64_t q = buf; q < blocks; q += 2) {
         if (!mbar_wait(bars.full(stage), phase)) break;
         const uint32_t a_addr = ring + kF8Stage * stage;
-        const uint64_t a_desc = sw128_desc(a_addr), b_desc = sw128_desc(a_addr + kABytes + kBBytes / 2 * h);
-        if (!mbar_wait(bars.free(buf, h), buf_phase ^ 1u)) break;
+        const uint64_t a_desc = sw128_desc(a_addr), b_desc = sw128_desc(a_addr + kABytes);
+        if (!mbar_wait(bars.free(buf), buf_phase ^ 1u)) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)           // 32 e4m3 along k = 32 bytes inside the swizzle row
-          tc_mma_f8(tmem_base + 256u * buf + 128u * h, a_desc + 2u * ks, b_desc + 2u * ks, idesc, ks > 0 ? 1u : 0u);
-        tc_commit(bars.done(stage, h));
-        if (++stage == kF8Stages) {
-          stage = 0;
+          tc_mma_f8(tmem_base + 256u * buf, a_desc + 2u * ks, b_desc + 2u * ks, idesc, ks > 0 ? 1u : 0u);
+        tc_commit(bars.done(stage));
+        buf_phase ^= 1u;
+        stage += 2;
+        if (stage >= C::kStages) {
+          stage -= C::kStages;
           phase ^= 1u;
-        }
-        if (++buf == 2) {
-          buf = 0;
-          buf_phase ^= 1u;
         }
       }
    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8RegsSum));
     // sums: thread = token row (TMEM lane quarter warp % 4), half of the columns.
-    // Gate/up: half h holds the gates and the ups of units 64 h .. 64 h + 63.
+    // Gate/up: half h holds the gates (columns 64 h) and the ups (128 + 64 h) of units 64 h .. 64 h + 63.
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int r = quarter * 32 + lane;
-    uint8_t* const out_s = smem_raw + (bars.base + kF8BarBytes - raw) + (warp - 4) * kOutBytes;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    uint8_t* const out_s = smem_raw + (bars.base + kF8BarBytes - raw) + (warp - 4) * C::kOutBytes;
+    const uint32_t t_warp = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (kGateUp ? 64u : 128u) * half;
     const float* const slots_s = reinterpret_cast<const float*>(smem_raw + (slots - raw));
     int stage = 0, buf = 0, slot = 0;
     uint32_t phase = 0;
@@ -420,16 +427,16 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         const float s0 = __shfl_sync(0xffffffffu, kb < 32 ? wc[0] : wc[2], kb & 31);
         const float s1 = kGateUp ? __shfl_sync(0xffffffffu, kb < 32 ? wc[1] : wc[3], kb & 31) : s0;
-        if (!mbar_wait(bars.done(stage, half), phase)) { ok = false; break; }
+        if (!mbar_wait(bars.done(stage), phase)) { ok = false; break; }
         tc_fence_after();
         auto release = [&]() {           // the buffer's columns of this warp are in registers
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bars.free(buf, half));
+          if (lane == 0) mbar_arrive(bars.free(buf));
         };
         if (warp_live) {
           // the next 32 columns are on their way while these are added
-          const uint32_t t0 = tmem_base + lane_off + 256u * buf + 128u * half;
+          const uint32_t t0 = t_warp + 256u * buf;
           const float sa = slots_s[slot * (kScaleSlotBytes / 4) + srow];
           const uint64_t f0 = twice(sa * s0), f1 = twice(sa * s1);
           uint32_t v[2][32];
@@ -437,7 +444,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           tmem_wait_ld32(v[0]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            if (c < 3) tmem_ld32(t0 + 32u * (c + 1), v[(c + 1) & 1]);
+            if (c < 3) tmem_ld32(t0 + (kGateUp && c >= 1 ? 64u : 0u) + 32u * (c + 1), v[(c + 1) & 1]);
             const uint64_t f = c < 2 ? f0 : f1;
 #pragma unroll
             for (int i = 0; i < 16; ++i) fma2(acc[c][i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         }
         slot = (slot + 1) % kScaleSlots;
         buf ^= 1;
-        if (++stage == kF8Stages) {
+        if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -458,15 +465,16 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       const int out_rows = valid - quarter * 32;       // rows of this warp that exist (may be <= 0)
       const int64_t wrow = row0 + quarter * 32;
       if constexpr (kGateUp) {
-        float amax = 0.0f;
+        float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             acc[c][i].x = silu_mul(acc[c][i].x, acc[c + 2][i].x);
             acc[c][i].y = silu_mul(acc[c][i].y, acc[c + 2][i].y);
-            amax = fmaxf(amax, fmaxf(fabsf(acc[c][i].x), fabsf(acc[c][i].y)));
+            m[i & 3] = fmaxf(m[i & 3], fmaxf(fabsf(acc[c][i].x), fabsf(acc[c][i].y)));
           }
+        float amax = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
         amax_s[half][r] = amax;
         asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");      // the two halves of these rows
         amax = fmaxf(fmaxf(amax, amax_s[half ^ 1][r]), kF8AmaxMin);
@@ -481,38 +489,40 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                             pack_e4m3(a[4].x * q, a[4].y * q, a[5].x * q, a[5].y * q),
                             pack_e4m3(a[6].x * q, a[6].y * q, a[7].x * q, a[7].y * q));
         }
-        store_rows(out_s, o, static_cast<uint8_t*>(p.out) + wrow * p.ncols + n * 128 + half * 64, p.ncols, out_rows);
+        store_rows<4, C::kOutPitch>(out_s, o, static_cast<uint8_t*>(p.out) + wrow * p.ncols + n * 128 + half * 64, p.ncols, out_rows);
         if (live && half == 0) p.out_scale[n * p.ld + row] = __fdiv_rn(amax, kF8Max);
       } else {
         // the thread's 128 columns in fp16, scaled by the power of two that puts their largest in [2^14, 2^15)
-        float amax = kF8AmaxMin;
+        float m[4] = {kF8AmaxMin, kF8AmaxMin, kF8AmaxMin, kF8AmaxMin};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fmaxf(fabsf(acc[c][i].x), fabsf(acc[c][i].y)));
-        const uint32_t top = __float_as_uint(amax) & 0x7f800000u;
+          for (int i = 0; i < 16; ++i) m[i & 3] = fmaxf(m[i & 3], fmaxf(fabsf(acc[c][i].x), fabsf(acc[c][i].y)));
+        const uint32_t top = __float_as_uint(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]))) & 0x7f800000u;
         const float q = __uint_as_float((268u << 23) - top);
         uint8_t* dst = static_cast<uint8_t*>(p.out) + (wrow * p.ncols + n * 256 + half * 128) * 2;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint4 o[4];
+        for (int c = 0; c < 2; ++c) {
+          uint4 o[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 8; ++j) {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __half2 b = __floats2half2_rn(acc[c][4 * j + i].x * q, acc[c][4 * j + i].y * q);
+              const float2 a = acc[2 * c + j / 4][4 * (j % 4) + i];
+              const __half2 b = __floats2half2_rn(a.x * q, a.y * q);
               w[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
             o[j] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          store_rows(out_s, o, dst + 64 * c, 2 * p.ncols, out_rows);
+          store_rows<8, C::kOutPitch>(out_s, o, dst + 128 * c, 2 * p.ncols, out_rows);
         }
         if (live) p.out_scale[row * (p.ncols / 128) + 2 * n + half] = __uint_as_float(top - (14u << 23));
       }
     }
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -650,14 +660,15 @@ cudaError_t launch_fp8_gemm(const void* a, int64_t a_rows, const void* a_shared,
   CUtensorMap tm_a, tm_w, tm_as, tm_ws, tm_sc;
   if (!encode_2d(&tm_a, u8, 1, a, kdim, static_cast<uint64_t>(a_rows), kKBlock, 32) ||
       !encode_2d(&tm_as, u8, 1, a_shared, kdim, static_cast<uint64_t>(as_rows), kKBlock, 32) ||
-      !encode_2d(&tm_w, u8, 1, w, kdim, static_cast<uint64_t>(p.E) * p.w_rows, kKBlock, 64) ||
-      !encode_2d(&tm_ws, u8, 1, w_shared ? w_shared : w, kdim, static_cast<uint64_t>(p.w_rows), kKBlock, 64) ||
+      !encode_2d(&tm_w, u8, 1, w, kdim, static_cast<uint64_t>(p.E) * p.w_rows, kKBlock, 128) ||
+      !encode_2d(&tm_ws, u8, 1, w_shared ? w_shared : w, kdim, static_cast<uint64_t>(p.w_rows), kKBlock, 128) ||
       !encode_2d(&tm_sc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, scales, static_cast<uint64_t>(p.ld),
                  static_cast<uint64_t>(p.k_blocks), kScaleBox, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   auto kern = expert_fp8_kernel<kGateUp>;
-  const size_t smem = 1024 + static_cast<size_t>(kF8Stage) * kF8Stages + kF8BarBytes + kSumWarps * kOutBytes +
-                      kScaleSlots * kScaleSlotBytes;
+  using C = F8Cfg<kGateUp>;
+  const size_t smem = 1024 + static_cast<size_t>(kF8Stage) * C::kStages + kScaleSlots * kScaleSlotBytes + kF8BarBytes +
+                      kSumWarps * C::kOutBytes;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   // token blocks: at most one partial block per group that has rows
