@@ -82,18 +82,19 @@ struct F8Bars {
   __device__ __forceinline__ uint32_t holder() const { return base + 8u * (2 * kMaxF8Stages + 2); }
 };
 constexpr int kF8BarBytes = (8 * (2 * kMaxF8Stages + 3) + 15) / 16 * 16;
-// Output rows pass through shared memory, 64 (gate/up) or 128 bytes (down) of 32
-// rows at a time per summing warp, so that neighbouring lanes write whole
-// lines (a store takes a cycle for each line that it touches): with a thread
-// writing its own row 16 bytes at a time the stores of a down tile took 2.5 us
-// of its 7.  The 16 bytes between rows keep both ways free of bank conflicts.
-// The down projection pays for the larger buffers with a stage, of which it
-// needs fewer (four k blocks a tile).
+// Output rows pass through shared memory.  h8 (16 KB a tile): 64 bytes of 32
+// rows per summing warp, written by neighbouring lanes as whole sectors (a store
+// takes a cycle for each line that it touches); 80 bytes from row to row keep
+// both ways free of bank conflicts.  o (64 KB a tile): a warp's 32 rows of 128
+// columns as two 128-byte wide boxes that the TMA unit stores behind the next
+// tile's sums; stored by the warps they held the sums up for 2 us a tile (385
+// us instead of 235 without stores, 16384 tokens).  The down projection pays
+// for that buffer with a stage, of which it needs fewer.
 template <bool kGateUp>
 struct F8Cfg {
   static constexpr int kStages = kGateUp ? 4 : 3;
-  static constexpr int kOutPitch = kGateUp ? 80 : 144;
-  static constexpr int kOutBytes = 32 * kOutPitch;
+  static constexpr int kOutPitch = 80;
+  static constexpr int kOutBytes = kGateUp ? 32 * kOutPitch : 2 * 32 * 128;
 };
 // Row scales ride with the operands: the scales of a k block lie side by side
 // by row, and one TMA copy brings the tile's (132 from the 16-byte boundary at
@@ -166,23 +167,31 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return lo | (hi << 16);
 }
 
-// 16 V bytes of each of the warp's 32 rows (lane l holds row l's) to dst + l *
+// 64 bytes of each of the warp's 32 rows (lane l holds row l's) to dst + l *
 // pitch, l < rows, by way of the warp's shared-memory buffer.
-template <int V, int kOutPitch>
-__device__ __forceinline__ void store_rows(uint8_t* buf, const uint4 (&v)[V], uint8_t* dst, int64_t pitch, int rows) {
-  static_assert(V == 4 || V == 8, "lanes per row");
+template <int kOutPitch>
+__device__ __forceinline__ void store_rows(uint8_t* buf, const uint4 (&v)[4], uint8_t* dst, int64_t pitch, int rows) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < V; ++i) *reinterpret_cast<uint4*>(buf + lane * kOutPitch + 16 * i) = v[i];
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + lane * kOutPitch + 16 * i) = v[i];
   __syncwarp();
-  const int l0 = lane / V, piece = (lane % V) * 16;
+  const int l0 = lane / 4, piece = (lane % 4) * 16;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int l = 32 / V * i + l0;
+  for (int i = 0; i < 4; ++i) {
+    const int l = 8 * i + l0;
     const uint4 w = *reinterpret_cast<const uint4*>(buf + l * kOutPitch + piece);
     if (l < rows) *reinterpret_cast<uint4*>(dst + l * pitch + piece) = w;
   }
   __syncwarp();
+}
+
+// A 32 x 128 byte box in the swizzled layout of a TMA store (row l at 128 l,
+// its 16-byte piece i at place i ^ (l % 8)): the first `rows` rows to dst.
+__device__ __forceinline__ void store_box_rows(const uint8_t* box, uint8_t* dst, int64_t pitch, int rows) {
+  const int lane = threadIdx.x & 31, piece = lane % 8;
+  for (int l = lane / 8; l < rows; l += 4)
+    *reinterpret_cast<uint4*>(dst + l * pitch + piece * 16) =
+        *reinterpret_cast<const uint4*>(box + l * 128 + ((piece ^ (l & 7)) << 4));
 }
 
 // All threads: mt[g] = token blocks of the groups before g (mt[G] all of
@@ -277,7 +286,8 @@ template <bool kGateUp>
 __global__ void __launch_bounds__(kF8Threads, 1)
     expert_fp8_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_as, const __grid_constant__ CUtensorMap tm_ws,
-                      const __grid_constant__ CUtensorMap tm_sc, const Fp8Params p) {
+                      const __grid_constant__ CUtensorMap tm_sc, const __grid_constant__ CUtensorMap tm_o,
+                      const Fp8Params p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ int32_t mt_s[kF8Groups + 1];
   __shared__ int64_t off_s[kF8Groups + 1];
@@ -286,9 +296,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   using C = F8Cfg<kGateUp>;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
-  // ring, scale slots (a TMA copy lands on a multiple of 128 bytes), barriers, output rows
-  const uint32_t slots = ring + kF8Stage * C::kStages;
-  static_assert(kScaleSlotBytes % 128 == 0 && (kF8Stage * C::kStages) % 128 == 0, "alignment of a TMA copy's target");
+  // ring, output rows (boxes on multiples of 1024 bytes), scale slots (of 128), barriers
+  const uint32_t outs = ring + kF8Stage * C::kStages;
+  const uint32_t slots = outs + kSumWarps * C::kOutBytes;
+  static_assert(kScaleSlotBytes % 128 == 0 && kF8Stage % 1024 == 0 && C::kOutBytes % (kGateUp ? 16 : 1024) == 0 &&
+                    (kSumWarps * C::kOutBytes) % 128 == 0, "alignment of TMA copies");
   const F8Bars bars{slots + kScaleSlotBytes * kScaleSlots};
   uint8_t* const holder_ptr = smem_raw + (bars.holder() - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -363,10 +375,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       int stage = buf;
       uint32_t phase = 0, buf_phase = 0;
       for (int64_t q = buf; q < blocks; q += 2) {
-        if (!mbar_wait(bars.full(stage), phase)) break;
+        // free first: it says that the sums of block q - 2 are done, so that the stage's last use (q - 3 or before)
+        // is, and full cannot be one phase behind the one that is waited for, which would look complete
+        if (!mbar_wait(bars.free(buf), buf_phase ^ 1u) || !mbar_wait(bars.full(stage), phase)) break;
         const uint32_t a_addr = ring + kF8Stage * stage;
         const uint64_t a_desc = sw128_desc(a_addr), b_desc = sw128_desc(a_addr + kABytes);
-        if (!mbar_wait(bars.free(buf), buf_phase ^ 1u)) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)           // 32 e4m3 along k = 32 bytes inside the swizzle row
@@ -386,7 +399,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // Gate/up: half h holds the gates (columns 64 h) and the ups (128 + 64 h) of units 64 h .. 64 h + 63.
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int r = quarter * 32 + lane;
-    uint8_t* const out_s = smem_raw + (bars.base + kF8BarBytes - raw) + (warp - 4) * C::kOutBytes;
+    const uint32_t out_addr = outs + static_cast<uint32_t>((warp - 4) * C::kOutBytes);
+    uint8_t* const out_s = smem_raw + (out_addr - raw);
     const uint32_t t_warp = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (kGateUp ? 64u : 128u) * half;
     const float* const slots_s = reinterpret_cast<const float*>(smem_raw + (slots - raw));
     int stage = 0, buf = 0, slot = 0;
@@ -489,7 +503,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                             pack_e4m3(a[4].x * q, a[4].y * q, a[5].x * q, a[5].y * q),
                             pack_e4m3(a[6].x * q, a[6].y * q, a[7].x * q, a[7].y * q));
         }
-        store_rows<4, C::kOutPitch>(out_s, o, static_cast<uint8_t*>(p.out) + wrow * p.ncols + n * 128 + half * 64, p.ncols, out_rows);
+        store_rows<C::kOutPitch>(out_s, o, static_cast<uint8_t*>(p.out) + wrow * p.ncols + n * 128 + half * 64, p.ncols, out_rows);
         if (live && half == 0) p.out_scale[n * p.ld + row] = __fdiv_rn(amax, kF8Max);
       } else {
         // the thread's 128 columns in fp16, scaled by the power of two that puts their largest in [2^14, 2^15)
@@ -500,26 +514,39 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           for (int i = 0; i < 16; ++i) m[i & 3] = fmaxf(m[i & 3], fmaxf(fabsf(acc[c][i].x), fabsf(acc[c][i].y)));
         const uint32_t top = __float_as_uint(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]))) & 0x7f800000u;
         const float q = __uint_as_float((268u << 23) - top);
-        uint8_t* dst = static_cast<uint8_t*>(p.out) + (wrow * p.ncols + n * 256 + half * 128) * 2;
+        if (lane == 0) bulk_wait_read<0>();          // the buffer's last box has been read
+        __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint4 o[8];
+        for (int c = 0; c < 16; ++c) {
+          uint32_t w[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 a = acc[2 * c + j / 4][4 * (j % 4) + i];
-              const __half2 b = __floats2half2_rn(a.x * q, a.y * q);
-              w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            o[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 4; ++i) {
+            const float2 a = acc[c / 4][4 * (c % 4) + i];
+            const __half2 b = __floats2half2_rn(a.x * q, a.y * q);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          store_rows<8, C::kOutPitch>(out_s, o, dst + 128 * c, 2 * p.ncols, out_rows);
+          *reinterpret_cast<uint4*>(out_s + 4096 * (c / 8) + lane * 128 + (((c % 8) ^ (lane & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        const int col = n * 256 + half * 128;
+        if (out_rows >= 32) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_o, col, static_cast<int>(wrow), out_addr);
+            tma_store_2d(&tm_o, col + 64, static_cast<int>(wrow), out_addr + 4096u);
+            bulk_commit();
+          }
+        } else if (out_rows > 0) {
+          __syncwarp();
+          uint8_t* dst = static_cast<uint8_t*>(p.out) + (wrow * p.ncols + col) * 2;
+          store_box_rows(out_s, dst, 2 * p.ncols, out_rows);
+          store_box_rows(out_s + 4096, dst + 128, 2 * p.ncols, out_rows);
         }
         if (live) p.out_scale[row * (p.ncols / 128) + 2 * n + half] = __uint_as_float(top - (14u << 23));
       }
     }
+    if (!kGateUp && lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -560,16 +587,14 @@ __global__ void __launch_bounds__(256) gather_fp8_kernel(const uint4* __restrict
 #pragma unroll
   for (int i = 0; i < kGatherRows / 8; ++i) {
     const int r = warp + 8 * i;
-    if (r >= n) break;
-    const int64_t t = tok[r];
-    if (p0 + r < NK) {
-      const uint4* src = x8 + t * vecs;
-      uint4* dst = xp + (p0 + r) * vecs;
+    if (r >= n || p0 + r >= NK) break;
+    const uint4* src = x8 + static_cast<int64_t>(tok[r]) * vecs;
+    uint4* dst = xp + (p0 + r) * vecs;
 #pragma unroll 5
-      for (int c = lane; c < vecs; c += 32) dst[c] = __ldg(src + c);
-    }
-    for (int b = lane; b < k_blocks; b += 32) sc[b][r] = __ldg(xs + t * k_blocks + b);
+    for (int c = lane; c < vecs; c += 32) dst[c] = __ldg(src + c);
   }
+  for (int r = warp; r < n; r += 8)
+    for (int b = lane; b < k_blocks; b += 32) sc[b][r] = __ldg(xs + static_cast<int64_t>(tok[r]) * k_blocks + b);
   __syncthreads();
   for (int b = warp; b < k_blocks; b += 8)
     if (lane < n) st[b * ld + p0 + lane] = sc[b][lane];
@@ -657,14 +682,17 @@ cudaError_t launch_fp8_gemm(const void* a, int64_t a_rows, const void* a_shared,
                             const void* w_shared, const float* scales, const Fp8Params& p, cudaStream_t s) {
   const uint64_t kdim = static_cast<uint64_t>(p.k_blocks) * kKBlock;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  CUtensorMap tm_a, tm_w, tm_as, tm_ws, tm_sc;
+  CUtensorMap tm_a, tm_w, tm_as, tm_ws, tm_sc, tm_o;
   if (!encode_2d(&tm_a, u8, 1, a, kdim, static_cast<uint64_t>(a_rows), kKBlock, 32) ||
       !encode_2d(&tm_as, u8, 1, a_shared, kdim, static_cast<uint64_t>(as_rows), kKBlock, 32) ||
       !encode_2d(&tm_w, u8, 1, w, kdim, static_cast<uint64_t>(p.E) * p.w_rows, kKBlock, 128) ||
       !encode_2d(&tm_ws, u8, 1, w_shared ? w_shared : w, kdim, static_cast<uint64_t>(p.w_rows), kKBlock, 128) ||
       !encode_2d(&tm_sc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, scales, static_cast<uint64_t>(p.ld),
-                 static_cast<uint64_t>(p.k_blocks), kScaleBox, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
+                 static_cast<uint64_t>(p.k_blocks), kScaleBox, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      (!kGateUp && !encode_2d(&tm_o, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.out, static_cast<uint64_t>(p.ncols),
+                              static_cast<uint64_t>(p.NK + (p.shared ? p.N : 0)), 64, 32)))
     return cudaErrorInvalidValue;
+  if (kGateUp) tm_o = tm_a;            // not used
   auto kern = expert_fp8_kernel<kGateUp>;
   using C = F8Cfg<kGateUp>;
   const size_t smem = 1024 + static_cast<size_t>(kF8Stage) * C::kStages + kScaleSlots * kScaleSlotBytes + kF8BarBytes +
@@ -677,7 +705,7 @@ cudaError_t launch_fp8_gemm(const void* a, int64_t a_rows, const void* a_shared,
   const int64_t tiles = (rows / kTokRows + partial + p.shared) * p.n_tiles;
   const int64_t sms = device_sm_count();
   return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kF8Threads), smem, s,
-                    dim3(0, 0, 0), tm_a, tm_w, tm_as, tm_ws, tm_sc, p);
+                    dim3(0, 0, 0), tm_a, tm_w, tm_as, tm_ws, tm_sc, tm_o, p);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

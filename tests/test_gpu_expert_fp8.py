@@ -141,6 +141,8 @@ CASES = [
     (130, 512, 256, 2, 1, False, False), (129, 256, 128, 4, 3, True, True), (700, 1280, 256, 8, 2, True, True),
     (1500, 256, 512, 32, 16, False, False), (333, 2048, 512, 128, 8, False, False), (2000, 512, 128, 512, 6, True, False),
     (3001, 768, 256, 5, 2, True, False),
+    # several tiles per block: every barrier goes round many times
+    (20000, 256, 512, 6, 2, True, False), (4000, 2048, 256, 4, 2, False, False), (9000, 1024, 384, 3, 1, True, True),
 ]
 
 
