@@ -50,7 +50,7 @@ constexpr uint32_t kABytes = kTokRows * kKBlock;            // 16 KB
 constexpr uint32_t kBBytes = kWRows * kKBlock;              // 32 KB
 constexpr uint32_t kF8Stage = kABytes + kBBytes;
 constexpr int kSumWarps = 8;
-constexpr int kF8Threads = 128 + 32 * kSumWarps;            // warp 0 TMA, warps 1, 2 MMA, warps 4..11 sums
+constexpr int kF8Threads = 128 + 32 * kSumWarps;            // warp 0 TMA, warps 1, 2 MMA, warp 3 tiles, warps 4..11 sums
 // Register split: a launch of 384 threads has 168 each, 64,512 in all; the
 // first warpgroup keeps 56 and the two summing ones take 224 (128 sums and two
 // 32-column loads): 128 * 56 + 256 * 224 = 64,512.
@@ -73,15 +73,18 @@ struct Fp8Params {
 
 // full(s): the operands of stage s are there.  done(s): the MMAs on stage s are
 // complete, which frees the stage and hands the buffer to the sums.  free(b):
-// the sums have read TMEM buffer b.
+// the sums have read TMEM buffer b.  tile(t), told(t): slot t holds the next
+// tile's place and weight scales, the sums are through with them.
 struct F8Bars {
   uint32_t base;
   __device__ __forceinline__ uint32_t full(int s) const { return base + 8u * s; }
   __device__ __forceinline__ uint32_t done(int s) const { return base + 8u * (kMaxF8Stages + s); }
   __device__ __forceinline__ uint32_t free(int b) const { return base + 8u * (2 * kMaxF8Stages + b); }
-  __device__ __forceinline__ uint32_t holder() const { return base + 8u * (2 * kMaxF8Stages + 2); }
+  __device__ __forceinline__ uint32_t tile(int t) const { return base + 8u * (2 * kMaxF8Stages + 2 + t); }
+  __device__ __forceinline__ uint32_t told(int t) const { return base + 8u * (2 * kMaxF8Stages + 4 + t); }
+  __device__ __forceinline__ uint32_t holder() const { return base + 8u * (2 * kMaxF8Stages + 6); }
 };
-constexpr int kF8BarBytes = (8 * (2 * kMaxF8Stages + 3) + 15) / 16 * 16;
+constexpr int kF8BarBytes = (8 * (2 * kMaxF8Stages + 7) + 15) / 16 * 16;
 // Output rows pass through shared memory.  h8 (16 KB a tile): 64 bytes of 32
 // rows per summing warp, written by neighbouring lanes as whole sectors (a store
 // takes a cycle for each line that it touches); 80 bytes from row to row keep
@@ -98,12 +101,13 @@ struct F8Cfg {
 };
 // Row scales ride with the operands: the scales of a k block lie side by side
 // by row, and one TMA copy brings the tile's (132 from the 16-byte boundary at
-// or below its first row) into one of eight slots.  A slot is overwritten eight
-// blocks later, when the MMAs of block + 4 (or + 5) are done, which wait for the
-// sums of block + 2: no barrier of its own.  Loaded by the summing threads one block
-// ahead, these 4-byte loads waited behind the bulk loads' queue: 538 us
+// or below its first row) into one of six slots.  A slot is overwritten six
+// blocks later, when the MMAs of block + 2 (or + 3) are done, which wait for the
+// sums of this block: no barrier of its own.  Loaded by the summing threads one
+// block ahead, these 4-byte loads waited behind the bulk loads' queue: 538 us
 // instead of the layer's 374 without sums (16384 tokens).
-constexpr int kScaleSlots = 8;
+constexpr int kScaleSlots = 6;
+constexpr int kMaxKBlocks = 64;          // d, F <= 8192
 constexpr uint32_t kScaleBox = 132;
 constexpr uint32_t kScaleSlotBytes = 640;
 
@@ -146,6 +150,11 @@ __device__ __forceinline__ void fma2(float2& acc, uint32_t v0, uint32_t v1, uint
   uint64_t a = *reinterpret_cast<uint64_t*>(&acc);
   asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(a) : "r"(v0), "r"(v1), "l"(ff));
   acc = *reinterpret_cast<float2*>(&a);
+}
+__device__ __forceinline__ float2 mul2(uint32_t v0, uint32_t v1, uint64_t ff) {
+  uint64_t a;
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tmul.rn.f32x2 %0, v, %3;\n\t}" : "=l"(a) : "r"(v0), "r"(v1), "l"(ff));
+  return *reinterpret_cast<float2*>(&a);
 }
 __device__ __forceinline__ uint64_t twice(float f) {
   uint64_t r;
@@ -293,6 +302,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   __shared__ int64_t off_s[kF8Groups + 1];
   __shared__ int32_t warp_tot[kF8Threads / 32];
   __shared__ float amax_s[2][kTokRows];
+  __shared__ int4 tile_s[2];                          // first row, rows that exist (0: no more tiles), feature block
+  __shared__ float ws_s[2][2][kMaxKBlocks];           // its weight scales by k block, two blocks of weight rows
   using C = F8Cfg<kGateUp>;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
@@ -311,7 +322,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_init(bars.full(s), 1);
       mbar_init(bars.done(s), 1);
     }
-    for (int b = 0; b < 2; ++b) mbar_init(bars.free(b), kSumWarps);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bars.free(b), kSumWarps);
+      mbar_init(bars.tile(b), 1);
+      mbar_init(bars.told(b), kSumWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -392,6 +407,45 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           phase ^= 1u;
         }
       }
+   } else if (warp == 3) {
+      // The tiles' places and weight scales for the sums, a tile ahead: worked out by the summing warps they cost
+      // each tile a thousand cycles.
+      const int wblocks = p.w_rows / 128;
+      int t = 0;
+      uint32_t phase = 0;
+      F8Walk walk(mt_s, off_s, G, p.n_tiles);
+      while (true) {
+        const bool more = walk.valid();
+        float w[kMaxKBlocks / 32][2];
+        int4 place = make_int4(0, 0, 0, 0);
+        if (more) {
+          const float* w0 = (walk.g == p.E ? p.ws_scale : p.w_scale + static_cast<int64_t>(walk.g) * wblocks * p.k_blocks) +
+                            static_cast<int64_t>(kGateUp ? walk.n : 2 * walk.n) * p.k_blocks;
+          const float* w1 = w0 + static_cast<int64_t>(kGateUp ? wblocks / 2 : 1) * p.k_blocks;
+#pragma unroll
+          for (int i = 0; i < kMaxKBlocks / 32; ++i) {
+            const int kb = lane + 32 * i;
+            w[i][0] = kb < p.k_blocks ? __ldg(w0 + kb) : 0.0f;
+            w[i][1] = kb < p.k_blocks ? __ldg(w1 + kb) : 0.0f;
+          }
+          place = make_int4(static_cast<int>(walk.row0()), walk.rows(), walk.n, 0);
+        }
+        if (!mbar_wait(bars.told(t), phase ^ 1u)) break;
+#pragma unroll
+        for (int i = 0; i < kMaxKBlocks / 32; ++i) {
+          ws_s[t][0][lane + 32 * i] = w[i][0];
+          ws_s[t][1][lane + 32 * i] = w[i][1];
+        }
+        if (lane == 0) tile_s[t] = place;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.tile(t));
+        if (!more) break;
+        walk.step();
+        if (++t == 2) {
+          t = 0;
+          phase ^= 1u;
+        }
+      }
    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8RegsSum));
@@ -403,44 +457,21 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     uint8_t* const out_s = smem_raw + (out_addr - raw);
     const uint32_t t_warp = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + (kGateUp ? 64u : 128u) * half;
     const float* const slots_s = reinterpret_cast<const float*>(smem_raw + (slots - raw));
-    int stage = 0, buf = 0, slot = 0;
-    uint32_t phase = 0;
+    int stage = 0, buf = 0, slot = 0, t = 0;
+    uint32_t phase = 0, tile_phase = 0;
     bool ok = true;
-    // the weight scales of a tile: lane l holds those of k blocks l and 32 + l, fetched a tile ahead
-    const int wblocks = p.w_rows / 128;
-    float wn[4] = {0.f, 0.f, 0.f, 0.f};
-    auto fetch = [&](int g, int n) {
-      const float* w0 = (g == p.E ? p.ws_scale : p.w_scale + static_cast<int64_t>(g) * wblocks * p.k_blocks) +
-                        (kGateUp ? n : 2 * n + half) * p.k_blocks;
-      const float* w1 = w0 + (wblocks / 2) * p.k_blocks;
-      if (lane < p.k_blocks) {
-        wn[0] = __ldg(w0 + lane);
-        if (kGateUp) wn[1] = __ldg(w1 + lane);
-      }
-      if (lane + 32 < p.k_blocks) {
-        wn[2] = __ldg(w0 + lane + 32);
-        if (kGateUp) wn[3] = __ldg(w1 + lane + 32);
-      }
-    };
-    F8Walk walk(mt_s, off_s, G, p.n_tiles);
-    if (walk.valid()) fetch(walk.g, walk.n);
-    while (walk.valid() && ok) {
-      const int n = walk.n, valid = walk.rows();
-      const int64_t row0 = walk.row0();
+    while (true) {
+      if (!mbar_wait(bars.tile(t), tile_phase)) break;
+      const int4 place = tile_s[t];
+      const int n = place.z, valid = place.y;
+      if (valid == 0) break;
+      const int64_t row0 = place.x;
       const bool live = r < valid, warp_live = quarter * 32 < valid;
       const int64_t row = row0 + r;
-      const int srow = static_cast<int>(row0 & 3) + r;
-      const float wc[4] = {wn[0], wn[1], wn[2], wn[3]};
-      walk.step();
-      if (walk.valid()) fetch(walk.g, walk.n);
+      const int srow = (place.x & 3) + r;
+      const float* const w0 = ws_s[t][kGateUp ? 0 : half];
       float2 acc[4][16];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
       for (int kb = 0; kb < p.k_blocks; ++kb) {
-        const float s0 = __shfl_sync(0xffffffffu, kb < 32 ? wc[0] : wc[2], kb & 31);
-        const float s1 = kGateUp ? __shfl_sync(0xffffffffu, kb < 32 ? wc[1] : wc[3], kb & 31) : s0;
         if (!mbar_wait(bars.done(stage), phase)) { ok = false; break; }
         tc_fence_after();
         auto release = [&]() {           // the buffer's columns of this warp are in registers
@@ -452,7 +483,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           // the next 32 columns are on their way while these are added
           const uint32_t t0 = t_warp + 256u * buf;
           const float sa = slots_s[slot * (kScaleSlotBytes / 4) + srow];
-          const uint64_t f0 = twice(sa * s0), f1 = twice(sa * s1);
+          const uint64_t f0 = twice(sa * w0[kb]), f1 = kGateUp ? twice(sa * w0[kMaxKBlocks + kb]) : f0;
           uint32_t v[2][32];
           tmem_ld32(t0, v[0]);
           tmem_wait_ld32(v[0]);
@@ -461,7 +492,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             if (c < 3) tmem_ld32(t0 + (kGateUp && c >= 1 ? 64u : 0u) + 32u * (c + 1), v[(c + 1) & 1]);
             const uint64_t f = c < 2 ? f0 : f1;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) fma2(acc[c][i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
+            for (int i = 0; i < 16; ++i) {
+              if (kb == 0) acc[c][i] = mul2(v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
+              else fma2(acc[c][i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
+            }
             if (c < 3) tmem_wait_ld32(v[(c + 1) & 1]);
             if (c == 2) release();
           }
@@ -476,6 +510,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         }
       }
       if (!ok) break;
+      if (lane == 0) mbar_arrive(bars.told(t));
+      t ^= 1;
+      tile_phase ^= t == 0 ? 1u : 0u;
       const int out_rows = valid - quarter * 32;       // rows of this warp that exist (may be <= 0)
       const int64_t wrow = row0 + quarter * 32;
       if constexpr (kGateUp) {
@@ -513,7 +550,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) m[i & 3] = fmaxf(m[i & 3], fmaxf(fabsf(acc[c][i].x), fabsf(acc[c][i].y)));
         const uint32_t top = __float_as_uint(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]))) & 0x7f800000u;
-        const float q = __uint_as_float((268u << 23) - top);
+        const uint64_t qq = twice(__uint_as_float((268u << 23) - top));
         if (lane == 0) bulk_wait_read<0>();          // the buffer's last box has been read
         __syncwarp();
 #pragma unroll
@@ -521,8 +558,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 a = acc[c / 4][4 * (c % 4) + i];
-            const __half2 b = __floats2half2_rn(a.x * q, a.y * q);
+            const float2 a0 = acc[c / 4][4 * (c % 4) + i];
+            const float2 a = mul2(__float_as_uint(a0.x), __float_as_uint(a0.y), qq);
+            const __half2 b = __floats2half2_rn(a.x, a.y);
             w[i] = *reinterpret_cast<const uint32_t*>(&b);
           }
           *reinterpret_cast<uint4*>(out_s + 4096 * (c / 8) + lane * 128 + (((c % 8) ^ (lane & 7)) << 4)) =
