@@ -679,20 +679,37 @@ _TYPE = {torch.bfloat16: KOLIBRI_TYPE_BF16, torch.float32: KOLIBRI_TYPE_F32}
 
 
 def _on_current(t, name):
-    """The library launches on the current device: refuse a tensor of another one."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    """The library launches on the current device: refuse a tensor of another one.  Returns the device's index."""
+    index = t.get_device()
+    if index < 0 or index != torch.cuda.current_device():
         raise ValueError(f"{name}: expected a tensor on the current CUDA device, got {t.device}")
+    return index
 
 
-def _need_all(dev, *args):
-    """_need for (tensor, dtype, shape, name) in turn, with one device for all; None tensors pass."""
+def _need_all(index, *args):
+    """_need for (tensor, dtype, shape, name) in turn, on the device `index`; None tensors pass."""
     for t, dtype, shape, name in args:
         if t is None:
             continue
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got "
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+            raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{index}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}"
                              f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _addr(t):
+    """The tensor's address for a pointer argument; None for NULL."""
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without a Stream object around it (0.1 us instead of 4.6)
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, index):
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_raw(index) if _current_raw else torch.cuda.current_stream(index).cuda_stream
 
 
 def _type_of(t, name):
@@ -712,7 +729,7 @@ def kolibri_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, res: tor
     scales [N, ceil(d/128)] fp32 or None); y8 * scales is the norm again.  res_out may be res (in place)."""
     N, d = x.shape
     dev = x.device
-    _on_current(x, "x")
+    index = _on_current(x, "x")
     xt, wt = _type_of(x, "x"), _type_of(weight, "weight")
     rt = 0 if res is None else _type_of(res, "res")
     if res is None:
@@ -727,13 +744,13 @@ def kolibri_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, res: tor
         y8 = torch.empty((N, d), dtype=torch.float8_e4m3fn, device=dev)
     if scales is None and y8 is not None:
         scales = torch.empty((N, groups), dtype=torch.float32, device=dev)
-    _need_all(dev, (x, x.dtype, (N, d), "x"), (weight, weight.dtype, (d,), "weight"),
+    _need_all(index, (x, x.dtype, (N, d), "x"), (weight, weight.dtype, (d,), "weight"),
               (res, None if res is None else res.dtype, (N, d), "res"),
               (res_out, None if res is None else res.dtype, (N, d), "res_out"), (y, torch.bfloat16, (N, d), "y"),
               (y8, torch.float8_e4m3fn, (N, d), "y8"), (scales, torch.float32, (N, groups), "scales"))
     _check("kolibri_rms_norm",
-           load().kolibri_rms_norm(_ptr(x), xt, _ptr(res), rt, _ptr(weight), wt, eps, N, d, _ptr(res_out), _ptr(y),
-                                   _ptr(y8), _ptr(scales), _stream(stream)))
+           load().kolibri_rms_norm(_addr(x), xt, _addr(res), rt, _addr(weight), wt, eps, N, d, _addr(res_out), _addr(y),
+                                   _addr(y8), _addr(scales), _raw_stream(stream, index)))
     return res_out, y, y8, scales
 
 
@@ -746,7 +763,7 @@ def kolibri_rms_norm_grad(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     Returns (gx [N, d] of h's type: the gradient of x and of res alike, gweight [d] fp32 or None)."""
     N, d = h.shape
     dev = h.device
-    _on_current(h, "h")
+    index = _on_current(h, "h")
     ht, gt, wt = _type_of(h, "h"), _type_of(gy, "gy"), _type_of(weight, "weight")
     if gx is None:
         gx = torch.empty_like(h)
@@ -755,12 +772,12 @@ def kolibri_rms_norm_grad(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     if ws is None and gweight is not None:
         n = int(load().kolibri_rms_norm_grad_workspace_size(N, d))
         ws = torch.empty((max(n, 1),), dtype=torch.uint8, device=dev)
-    _need_all(dev, (h, h.dtype, (N, d), "h"), (gy, gy.dtype, (N, d), "gy"), (weight, weight.dtype, (d,), "weight"),
+    _need_all(index, (h, h.dtype, (N, d), "h"), (gy, gy.dtype, (N, d), "gy"), (weight, weight.dtype, (d,), "weight"),
               (gres, h.dtype, (N, d), "gres"), (gx, h.dtype, (N, d), "gx"), (gweight, torch.float32, (d,), "gweight"),
               (ws, torch.uint8, (0 if ws is None else ws.numel(),), "ws"))
     _check("kolibri_rms_norm_grad",
-           load().kolibri_rms_norm_grad(_ptr(gy), gt, _ptr(h), ht, _ptr(weight), wt, eps, _ptr(gres), N, d, _ptr(gx),
-                                        _ptr(gweight), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
+           load().kolibri_rms_norm_grad(_addr(gy), gt, _addr(h), ht, _addr(weight), wt, eps, _addr(gres), N, d, _addr(gx),
+                                        _addr(gweight), _addr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, index)))
     return gx, gweight
 
 
@@ -777,7 +794,7 @@ def kolibri_balance_loss(z: torch.Tensor, ids: torch.Tensor, lam: float, seq_off
     K = ids.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
     dev = z.device
-    _on_current(z, "z")
+    index = _on_current(z, "z")
     if gz is None and want_gz:
         if accumulate:
             raise ValueError("gz: accumulate needs the gradient to add to")
@@ -791,15 +808,15 @@ def kolibri_balance_loss(z: torch.Tensor, ids: torch.Tensor, lam: float, seq_off
     if ws is None:
         n = int(load().kolibri_balance_loss_workspace_size(N, E, S))
         ws = torch.empty((max(n, 1),), dtype=torch.uint8, device=dev)
-    _need_all(dev, (z, torch.float32, (N, E), "z"), (ids, torch.int32, (N, K), "ids"),
+    _need_all(index, (z, torch.float32, (N, E), "z"), (ids, torch.int32, (N, K), "ids"),
               (seq_offsets, torch.int64, (S + 1,), "seq_offsets"), (grad_loss, torch.float32, (S,), "grad_loss"),
               (gz, torch.float32, (N, E), "gz"), (loss, torch.float32, (S,), "loss"),
               (counts, torch.int32, (S, E), "counts"), (prob, torch.float32, (S, E), "prob"),
               (ws, torch.uint8, (ws.numel(),), "ws"))
     _check("kolibri_balance_loss",
-           load().kolibri_balance_loss(_ptr(z), _ptr(ids), _ptr(seq_offsets), N, E, K, S, score, lam, _ptr(grad_loss),
-                                       1 if accumulate else 0, _ptr(loss), _ptr(counts), _ptr(prob), _ptr(gz), _ptr(ws),
-                                       ws.numel(), _stream(stream)))
+           load().kolibri_balance_loss(_addr(z), _addr(ids), _addr(seq_offsets), N, E, K, S, score, lam, _addr(grad_loss),
+                                       1 if accumulate else 0, _addr(loss), _addr(counts), _addr(prob), _addr(gz), _addr(ws),
+                                       ws.numel(), _raw_stream(stream, index)))
     return loss, counts, prob, gz
 
 
@@ -811,17 +828,17 @@ def kolibri_balance_loss_grad(z: torch.Tensor, counts: torch.Tensor, K: int, lam
     N, E = z.shape
     S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
     dev = z.device
-    _on_current(z, "z")
+    index = _on_current(z, "z")
     if gz is None:
         if accumulate:
             raise ValueError("gz: accumulate needs the gradient to add to")
         gz = torch.empty((N, E), dtype=torch.float32, device=dev)
-    _need_all(dev, (z, torch.float32, (N, E), "z"), (counts, torch.int32, (S, E), "counts"),
+    _need_all(index, (z, torch.float32, (N, E), "z"), (counts, torch.int32, (S, E), "counts"),
               (seq_offsets, torch.int64, (S + 1,), "seq_offsets"), (grad_loss, torch.float32, (S,), "grad_loss"),
               (gz, torch.float32, (N, E), "gz"))
     _check("kolibri_balance_loss_grad",
-           load().kolibri_balance_loss_grad(_ptr(z), _ptr(counts), _ptr(seq_offsets), N, E, K, S, score, lam,
-                                            _ptr(grad_loss), 1 if accumulate else 0, _ptr(gz), _stream(stream)))
+           load().kolibri_balance_loss_grad(_addr(z), _addr(counts), _addr(seq_offsets), N, E, K, S, score, lam,
+                                            _addr(grad_loss), 1 if accumulate else 0, _addr(gz), _raw_stream(stream, index)))
     return gz
 
 
@@ -847,7 +864,7 @@ def kolibri_expert_ffn_fp8(x8: torch.Tensor, x_scale: torch.Tensor, perm: torch.
     E, F2, _ = w_gate_up.shape
     F = F2 // 2
     dev = x8.device
-    _on_current(x8, "x8")
+    index = _on_current(x8, "x8")
     shared = ws_gate_up is not None
     if any((t is not None) != shared for t in (ss_gate_up, ws_down, ss_down)):
         raise ValueError("shared expert: ws_gate_up, ss_gate_up, ws_down and ss_down go together")
@@ -856,7 +873,7 @@ def kolibri_expert_ffn_fp8(x8: torch.Tensor, x_scale: torch.Tensor, perm: torch.
     if ws is None:
         ws = expert_ffn_fp8_workspace(N, d, F, K, shared, dev)
     f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
-    _need_all(dev, (x8, f8, (N, d), "x8"), (x_scale, f32, (N, d // 128), "x_scale"), (perm, i32, (N * K,), "perm"),
+    _need_all(index, (x8, f8, (N, d), "x8"), (x_scale, f32, (N, d // 128), "x_scale"), (perm, i32, (N * K,), "perm"),
               (offsets, torch.int64, (E + 1,), "offsets"), (inv, i32, (N * K,), "inv"), (gates, f32, (N, K), "gates"),
               (w_gate_up, f8, (E, 2 * F, d), "w_gate_up"), (s_gate_up, f32, (E, 2 * F // 128, d // 128), "s_gate_up"),
               (w_down, f8, (E, d, F), "w_down"), (s_down, f32, (E, d // 128, F // 128), "s_down"),
@@ -865,7 +882,7 @@ def kolibri_expert_ffn_fp8(x8: torch.Tensor, x_scale: torch.Tensor, perm: torch.
               (y, torch.bfloat16, (N, d), "y"), (ws, torch.uint8, (ws.numel(),), "ws"))
     _check("kolibri_expert_ffn_fp8",
            load().kolibri_expert_ffn_fp8(
-               _ptr(x8), _ptr(x_scale), _ptr(perm), _ptr(offsets), _ptr(inv), _ptr(gates), _ptr(w_gate_up),
-               _ptr(s_gate_up), _ptr(w_down), _ptr(s_down), _ptr(ws_gate_up), _ptr(ss_gate_up), _ptr(ws_down),
-               _ptr(ss_down), _ptr(y), N, d, F, E, K, _ptr(ws), ws.numel(), _stream(stream)))
+               _addr(x8), _addr(x_scale), _addr(perm), _addr(offsets), _addr(inv), _addr(gates), _addr(w_gate_up),
+               _addr(s_gate_up), _addr(w_down), _addr(s_down), _addr(ws_gate_up), _addr(ss_gate_up), _addr(ws_down),
+               _addr(ss_down), _addr(y), N, d, F, E, K, _addr(ws), ws.numel(), _raw_stream(stream, index)))
     return y

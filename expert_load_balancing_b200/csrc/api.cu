@@ -555,7 +555,7 @@ kolibri_status kolibri_device_status(void* stream) {
                      status_take_permute() | status_take_route() | status_take_logits() |
                      status_take_forward() | status_take_balance() | status_take_small() |
                      status_take_experts() | status_take_decode() | status_take_balance_loss() |
-                     status_take_expert_fp8();
+                     status_take_expert_fp8() | status_take_expert_fp8_decode();
   if (v & kStatusReadFailed) return KOLIBRI_ERR_CUDA;
   if (v & kStatusTimeout) return KOLIBRI_ERR_TIMEOUT;
   if (v & kStatusBadInput) return KOLIBRI_ERR_DEVICE;

@@ -778,11 +778,14 @@ bool expert_fp8_shape_supported(int32_t d, int32_t F, int32_t E) {
 }
 
 size_t expert_fp8_ws_bytes(int64_t N, int32_t d, int32_t F, int32_t K, bool shared) {
-  return fp8_layout(N, d, F, K, shared).total;
+  const Fp8Layout L = fp8_layout(N, d, F, K, shared);
+  const size_t decode = static_cast<size_t>(L.rows) * F * sizeof(float);      // h in fp32
+  return expert_fp8_decode_preferred(N, K, shared) && decode > L.total ? decode : L.total;
 }
 
 cudaError_t launch_expert_ffn_fp8(const ExpertFp8Args& a, cudaStream_t s) {
   const bool shared = a.ws_gate_up != nullptr;
+  if (expert_fp8_decode_preferred(a.N, a.K, shared)) return launch_expert_ffn_fp8_decode(a, s);
   const Fp8Layout L = fp8_layout(a.N, a.d, a.F, a.K, shared);
   char* base = static_cast<char*>(a.ws);
   const int64_t NK = a.N * a.K;

@@ -205,6 +205,10 @@ struct ExpertFp8Args {
 bool expert_fp8_shape_supported(int32_t d, int32_t F, int32_t E);
 size_t expert_fp8_ws_bytes(int64_t N, int32_t d, int32_t F, int32_t K, bool shared);
 cudaError_t launch_expert_ffn_fp8(const ExpertFp8Args& a, cudaStream_t s);
+// Few tokens (expert_fp8_decode.cu): up to this many rows, shared ones included.
+constexpr int64_t kFp8DecodeSlots = 64;
+bool expert_fp8_decode_preferred(int64_t N, int32_t K, bool shared);
+cudaError_t launch_expert_ffn_fp8_decode(const ExpertFp8Args& a, cudaStream_t s);
 
 // norm.cu: the norm in front of the router and its gradient.
 cudaError_t launch_rms_norm(const void* x, int x_type, const void* res, int res_type, const void* weight,
@@ -264,5 +268,6 @@ unsigned status_take_experts();
 unsigned status_take_decode();
 unsigned status_take_balance_loss();
 unsigned status_take_expert_fp8();
+unsigned status_take_expert_fp8_decode();
 
 }  // namespace kolibri

@@ -75,7 +75,15 @@ def _wide(w, s):
     return w.double() * s.double().repeat_interleave(128, -2).repeat_interleave(128, -1)
 
 
+DECODE_ROWS = 64      # up to this many rows h stays in fp32 and is put into e4m3 where it is read
+
+
 def _hidden(ws, rows, F):
+    if rows <= DECODE_ROWS:
+        h = ws[:rows * F * 4].view(torch.float32).view(rows, F // 128, 128)
+        amax = h.abs().amax(2).clamp_min(1e-30)
+        q = (h * (448.0 / amax)[..., None]).clamp(-448, 448).to(F8)          # the same fp32 operations, the same bits
+        return q.view(rows, F), amax / 448.0
     h8 = ws[:rows * F].view(F8).view(rows, F)
     at = (rows * F + 255) // 256 * 256
     ld = max((rows + 3) // 4 * 4, 132)
@@ -141,6 +149,7 @@ CASES = [
     (130, 512, 256, 2, 1, False, False), (129, 256, 128, 4, 3, True, True), (700, 1280, 256, 8, 2, True, True),
     (1500, 256, 512, 32, 16, False, False), (333, 2048, 512, 128, 8, False, False), (2000, 512, 128, 512, 6, True, False),
     (3001, 768, 256, 5, 2, True, False),
+    (1, 8192, 128, 4, 2, True, False), (1, 256, 8192, 4, 1, True, False), (260, 4352, 128, 4, 1, False, False), (150, 256, 4224, 4, 1, True, False),
     # several tiles per block: every barrier goes round many times
     (20000, 256, 512, 6, 2, True, False), (4000, 2048, 256, 4, 2, False, False), (9000, 1024, 384, 3, 1, True, True),
 ]
@@ -218,6 +227,30 @@ def test_bad_entries_are_reported():
         c["off"][i] = v
         _call(c)
         assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, (i, v)
+    check_status()
+
+
+def test_bad_entries_are_reported_for_a_few_tokens():
+    for bad in (-7, 8 * 2):
+        c = _case(8, 256, 128, 8, 2, True, 5)
+        c["inv"][13] = bad
+        _call(c)
+        assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, bad
+    for i, v in ((0, 1), (8, 15), (8, 1 << 40), (4, -1), (4, 1 << 35)):
+        c = _case(8, 256, 128, 8, 2, False, 5)
+        c["off"][i] = v
+        _call(c)
+        assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, (i, v)
+    check_status()
+
+
+@pytest.mark.parametrize("N,K,shared", [(9, 6, True), (10, 6, True), (64, 1, False), (65, 1, False), (4, 16, False), (3, 16, True)])
+def test_both_sides_of_the_choice_of_kernels(N, K, shared):
+    """Up to 64 rows the layer streams each row's weights, above it runs in tiles."""
+    c = _case(N, 512, 384, 20, K, shared, 40 + N)
+    ws = B.expert_ffn_fp8_workspace(N, 512, 384, K, shared)
+    ws.fill_(255)
+    _check(c, _call(c, ws=ws), ws)
     check_status()
 
 
