@@ -38,8 +38,10 @@ namespace {
 
 constexpr int kLossWarps = 8;
 constexpr int kLossThreads = 32 * kLossWarps;
-constexpr int kLossBlocksPerSm = 4;
+constexpr int kCountAhead = 8;           // ids in flight per thread of the counting pass
 constexpr int kMaxE = KOLIBRI_MAX_EXPERTS;
+
+constexpr int kSeqCache = 1024;
 
 // Sequence boundaries: seq[0..S] (or null: one sequence of all rows), cut to
 // [0, N] so that no index leaves the arrays whatever the caller wrote.
@@ -47,6 +49,14 @@ struct Seqs {
   const int64_t* seq;
   int64_t N;
   int S;
+  // The same boundaries read from shared memory, if they fit: the search for a
+  // block's first sequence is a chain of dependent loads.
+  __device__ __forceinline__ Seqs cached(int64_t* buf) const {
+    if (!seq || S >= kSeqCache) return *this;
+    for (int s = threadIdx.x; s <= S; s += blockDim.x) buf[s] = seq[s];
+    __syncthreads();
+    return Seqs{buf, N, S};
+  }
   __device__ __forceinline__ int64_t at(int s) const {
     if (!seq) return s == 0 ? 0 : N;
     const int64_t v = seq[s];
@@ -65,9 +75,11 @@ struct Seqs {
 };
 
 // counts [S][E] += the slots of this block's rows.  counts is zero on entry.
-__global__ void __launch_bounds__(kLossThreads) seq_count_kernel(const int32_t* ids, Seqs q, int E, int K,
+__global__ void __launch_bounds__(kLossThreads) seq_count_kernel(const int32_t* ids, Seqs given, int E, int K,
                                                                  int64_t chunk, int32_t* counts) {
   __shared__ int32_t hist[kMaxE];
+  __shared__ int64_t seq_s[kSeqCache];
+  const Seqs q = given.cached(seq_s);
   const int64_t r0 = blockIdx.x * chunk;
   const int64_t r1 = r0 + chunk < q.N ? r0 + chunk : q.N;
   for (int e = threadIdx.x; e < E; e += kLossThreads) hist[e] = 0;
@@ -82,10 +94,18 @@ __global__ void __launch_bounds__(kLossThreads) seq_count_kernel(const int32_t* 
     if (b >= r1) break;
     const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
     if (lo >= hi) continue;
-    for (int64_t j = lo * K + threadIdx.x; j < hi * K; j += kLossThreads) {
-      const int32_t e = ids[j];
-      if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-      else raise_status(kStatusBadInput);
+    const int64_t j1 = hi * K;
+    for (int64_t j = lo * K + threadIdx.x; j < j1; j += kCountAhead * kLossThreads) {
+      int32_t e[kCountAhead];
+#pragma unroll
+      for (int i = 0; i < kCountAhead; ++i)
+        if (j + i * kLossThreads < j1) e[i] = __ldcs(ids + j + i * kLossThreads);
+#pragma unroll
+      for (int i = 0; i < kCountAhead; ++i)
+        if (j + i * kLossThreads < j1) {
+          if (e[i] >= 0 && e[i] < E) atomicAdd(&hist[e[i]], 1);
+          else raise_status(kStatusBadInput);
+        }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kLossThreads) {
@@ -113,39 +133,54 @@ struct LossParams {
   double lambda;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// 2^x and 1 / x by the hardware's approximations, subnormal results flushed:
+// 2^-22 relative each, and the product with log2 e adds 2^-24 |z - c|; far below
+// the 2^-24 sqrt(T) of the sums they enter.  (c is subtracted first: folded into
+// one multiply-add it would cost 2^-24 of |z| for logits far from zero.)
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// e^x by the hardware's base-2 exponential: about 2^-22 + |x| 2^-24 relative,
-// far below the 2^-24 sqrt(T) of the sums it enters; e^-inf = 0.
-__device__ __forceinline__ float fast_exp(float x) { return __expf(x); }
-
-// A warp per row; lane l holds the float4s l, l + 32, ... (V of them) of the
-// row's E logits.
+// L lanes per row (8, 16 or 32): lane l of them holds the float4s l, l + L, ...
+// (V of them) of the row's E logits.  Narrow rows share a warp, so that a row's
+// reductions cost it a share of the shuffles only: a warp per row of 128 logits
+// spent 149 instructions a row, most of them there (E = 128, 65,536 rows in 61
+// sequences, loss and gradient apart: 46 us).
 //
 // Sigmoid scores are formed as q = 1 / (e^c + e^(c - z)) = e^-c sigma(z) with c
 // = min(max_j z_j, 0): the common factor keeps rows whose logits are all far
 // below zero from vanishing.  1 - sigma(z) = q e^(c - z) where sigma > 1/2 and
 // 1 - q e^c elsewhere, both free of cancellation.  A row without a finite
 // logit gives p = 0 and gradient 0.
-template <int V, bool kSoftmax, bool kProb, bool kGrad>
-__global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossParams p) {
+//
+// Blocks per SM: the warps that wait for loads count (E = 384, 1M rows, loss
+// and gradient: 575 us at four blocks, 640 at two, 765 at the three of an
+// unbounded register count).
+template <int V>
+struct LossBlocks {
+  static constexpr int kPerSm = V <= 3 ? 4 : 2;
+};
+
+template <int L, int V, bool kSoftmax, bool kProb, bool kGrad>
+__global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_loss_kernel(const LossParams p) {
   __shared__ float psum[kProb ? kLossWarps * kMaxE : 1];
   __shared__ double dsum[kLossWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kRows = 32 / L;          // rows of a warp at once
+  const int lane = threadIdx.x & (L - 1), group = (threadIdx.x & 31) / L, warp = threadIdx.x >> 5;
   const int E4 = p.E >> 2;
-  const Seqs q = p.q;
+  __shared__ int64_t seq_s[kSeqCache];
   const int64_t r0 = blockIdx.x * p.chunk;
-  const int64_t r1 = r0 + p.chunk < q.N ? r0 + p.chunk : q.N;
+  const int64_t r1 = r0 + p.chunk < p.q.N ? r0 + p.chunk : p.q.N;
   pdl_wait();          // the counts
+  const Seqs q = p.q.cached(seq_s);
   if constexpr (kGrad) {
     // rows of the chunk before the first and behind the last sequence have no gradient
     if (!p.accumulate) {
@@ -162,65 +197,72 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossPa
     if (b >= r1) break;
     const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
     if (lo >= hi) continue;
-    const double T = static_cast<double>(e_ - b);
-    const double to_f = static_cast<double>(p.E) / (static_cast<double>(p.K) * T);
+    // f - 1 = (E c - K T) / (K T), the numerator an integer: exact where loads are even
+    const int64_t slots = (e_ - b) * p.K;
+    const float per_slot = __fdiv_rn(1.0f, static_cast<float>(slots));
     float fr[4 * V], acc[4 * V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int c4 = lane + 32 * j;
+      const int c4 = lane + L * j;
       int4 c = make_int4(0, 0, 0, 0);
       if (c4 < E4) c = reinterpret_cast<const int4*>(p.counts)[static_cast<int64_t>(s) * E4 + c4];
-      fr[4 * j + 0] = static_cast<float>(c.x * to_f - 1.0);
-      fr[4 * j + 1] = static_cast<float>(c.y * to_f - 1.0);
-      fr[4 * j + 2] = static_cast<float>(c.z * to_f - 1.0);
-      fr[4 * j + 3] = static_cast<float>(c.w * to_f - 1.0);
+      fr[4 * j + 0] = static_cast<float>(static_cast<int64_t>(c.x) * p.E - slots) * per_slot;
+      fr[4 * j + 1] = static_cast<float>(static_cast<int64_t>(c.y) * p.E - slots) * per_slot;
+      fr[4 * j + 2] = static_cast<float>(static_cast<int64_t>(c.z) * p.E - slots) * per_slot;
+      fr[4 * j + 3] = static_cast<float>(static_cast<int64_t>(c.w) * p.E - slots) * per_slot;
     }
 #pragma unroll
     for (int i = 0; i < 4 * V; ++i) acc[i] = 0.0f;
     float gscale = 0.0f;
     if constexpr (kGrad)
-      gscale = static_cast<float>(p.lambda / T * (p.grad_loss ? static_cast<double>(p.grad_loss[s]) : 1.0));
+      gscale = __fdiv_rn(static_cast<float>(p.lambda) * (p.grad_loss ? p.grad_loss[s] : 1.0f), static_cast<float>(e_ - b));
     double dot_sum = 0.0;
-    for (int64_t row = lo + warp; row < hi; row += kLossWarps) {
+    for (int64_t base = lo + warp * kRows; base < hi; base += kRows * kLossWarps) {
+      const int64_t row = base + group;
+      const bool there = row < hi;
       const float4* zr = reinterpret_cast<const float4*>(p.z) + row * E4;
       float z[4 * V], u[4 * V];
-      float m = -INFINITY;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int c4 = lane + 32 * j;
+        const int c4 = lane + L * j;
         float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (c4 < E4) v = __ldcs(zr + c4);
+        if (c4 < E4 && there) v = __ldcs(zr + c4);
         z[4 * j] = v.x; z[4 * j + 1] = v.y; z[4 * j + 2] = v.z; z[4 * j + 3] = v.w;
-        m = fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
       }
-      m = warp_max(m);
-      const bool none = m == -INFINITY;
+      float m = z[0];
+#pragma unroll
+      for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, z[i]);
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const bool none = m == -INFINITY;               // a row behind the last one is such a row too
       float sum = 0.0f, dot = 0.0f, ec = 1.0f;
       if constexpr (kSoftmax) {
         const float c = none ? 0.0f : m;
 #pragma unroll
-        for (int i = 0; i < 4 * V; ++i) {
-          z[i] = fast_exp(z[i] - c);
-          sum += z[i];
-          dot = fmaf(fr[i], z[i], dot);
-        }
+        for (int i = 0; i < 4 * V; ++i) z[i] = exp2_fast((z[i] - c) * kLog2e);
       } else {
         const float c = none ? 0.0f : fminf(m, 0.0f);
-        ec = fast_exp(c);
+        ec = exp2_fast(c * kLog2e);
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) {
-          u[i] = fast_exp(c - z[i]);
-          z[i] = __fdividef(1.0f, ec + u[i]);
-          sum += z[i];
-          dot = fmaf(fr[i], z[i], dot);
+          u[i] = exp2_fast((c - z[i]) * kLog2e);
+          z[i] = rcp_fast(ec + u[i]);
         }
       }
-      sum = warp_sum(sum);
-      dot = warp_sum(dot);
-      const float inv = none ? 0.0f : __fdividef(1.0f, sum);
+#pragma unroll
+      for (int i = 0; i < 4 * V; ++i) {
+        sum += z[i];
+        dot = fmaf(fr[i], z[i], dot);
+      }
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      }
+      const float inv = none ? 0.0f : rcp_fast(sum);
       dot = __fmul_rn(dot, inv);          // uncontracted: the same bits in every form of the pass
       if constexpr (kProb) {
-        dot_sum += none ? -1.0f : dot;     // a row without p adds nothing to L
+        dot_sum += !there ? 0.0f : none ? -1.0f : dot;         // a row without p adds nothing to L
 #pragma unroll
         for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
       }
@@ -229,7 +271,7 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossPa
         float4* gr = reinterpret_cast<float4*>(p.gz) + row * E4;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const int c4 = lane + 32 * j;
+          const int c4 = lane + L * j;
           float o[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -237,7 +279,7 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossPa
             o[i] = k * z[x] * (fr[x] - dot);
             if constexpr (!kSoftmax) o[i] *= u[x] < ec ? z[x] * u[x] : fmaf(-z[x], ec, 1.0f);
           }
-          if (c4 < E4) {
+          if (c4 < E4 && there) {
             if (p.accumulate) {
               const float4 old = gr[c4];
               o[0] += old.x; o[1] += old.y; o[2] += old.z; o[3] += old.w;
@@ -249,14 +291,21 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const LossPa
     }
     if constexpr (kProb) {
       const int64_t slot = blockIdx.x + s;
+      // the warp's rows at once, in a fixed order
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 4 * V; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        dot_sum += __shfl_xor_sync(0xffffffffu, dot_sum, o);
+      }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int c4 = lane + 32 * j;
-        if (c4 < E4)
+        const int c4 = lane + L * j;
+        if (c4 < E4 && group == 0)
           reinterpret_cast<float4*>(psum + warp * kMaxE)[c4] =
               make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
       }
-      if (lane == 0) dsum[warp] = dot_sum;
+      if (lane == 0 && group == 0) dsum[warp] = dot_sum;
       __syncthreads();
       for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
         float t = 0.0f;
@@ -319,8 +368,11 @@ __global__ void __launch_bounds__(32 * kFinishRows) balance_finish_kernel(const 
 struct LossPlan {
   int64_t chunk, chunks;
 };
-LossPlan loss_plan(int64_t N) {
-  const int64_t most = static_cast<int64_t>(device_sm_count()) * kLossBlocksPerSm;
+// One wave of blocks: a second one, of a few blocks, cost 65,536 rows of 128
+// half their time again.
+LossPlan loss_plan(int64_t N, int32_t E) {
+  const bool wide = (E > 64 && E <= 128) || (E > 192 && E <= 256) || E > 384;      // four float4s per lane
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * (wide ? LossBlocks<4>::kPerSm : LossBlocks<3>::kPerSm);
   LossPlan lp;
   lp.chunk = (N + most - 1) / most;
   lp.chunk = (lp.chunk + kLossWarps - 1) / kLossWarps * kLossWarps;
@@ -328,21 +380,22 @@ LossPlan loss_plan(int64_t N) {
   return lp;
 }
 
-template <int V, bool kSoftmax, bool kProb, bool kGrad>
-cudaError_t launch_loss_pass(const LossParams& p, int64_t chunks, cudaStream_t s) {
-  return launch_pdl(balance_loss_kernel<V, kSoftmax, kProb, kGrad>, dim3(static_cast<unsigned>(chunks)),
-                    dim3(kLossThreads), 0, s, dim3(0, 0, 0), p);
+template <int L, int V, bool kProb, bool kGrad>
+cudaError_t launch_loss_pass(const LossParams& p, int score, int64_t chunks, cudaStream_t s) {
+  auto kern = score == KOLIBRI_SCORE_SOFTMAX ? balance_loss_kernel<L, V, true, kProb, kGrad>
+                                             : balance_loss_kernel<L, V, false, kProb, kGrad>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(chunks)), dim3(kLossThreads), 0, s, dim3(0, 0, 0), p);
 }
 
+// The fewest lanes whose four float4s hold a row.
 template <bool kProb, bool kGrad>
 cudaError_t launch_loss_v(const LossParams& p, int score, int64_t chunks, cudaStream_t s) {
-  const bool soft = score == KOLIBRI_SCORE_SOFTMAX;
-  switch ((p.E + 127) / 128) {
-    case 1: return soft ? launch_loss_pass<1, true, kProb, kGrad>(p, chunks, s) : launch_loss_pass<1, false, kProb, kGrad>(p, chunks, s);
-    case 2: return soft ? launch_loss_pass<2, true, kProb, kGrad>(p, chunks, s) : launch_loss_pass<2, false, kProb, kGrad>(p, chunks, s);
-    case 3: return soft ? launch_loss_pass<3, true, kProb, kGrad>(p, chunks, s) : launch_loss_pass<3, false, kProb, kGrad>(p, chunks, s);
-    default: return soft ? launch_loss_pass<4, true, kProb, kGrad>(p, chunks, s) : launch_loss_pass<4, false, kProb, kGrad>(p, chunks, s);
-  }
+  if (p.E <= 64) return launch_loss_pass<8, 2, kProb, kGrad>(p, score, chunks, s);
+  if (p.E <= 128) return launch_loss_pass<8, 4, kProb, kGrad>(p, score, chunks, s);
+  if (p.E <= 192) return launch_loss_pass<16, 3, kProb, kGrad>(p, score, chunks, s);
+  if (p.E <= 256) return launch_loss_pass<16, 4, kProb, kGrad>(p, score, chunks, s);
+  if (p.E <= 384) return launch_loss_pass<32, 3, kProb, kGrad>(p, score, chunks, s);
+  return launch_loss_pass<32, 4, kProb, kGrad>(p, score, chunks, s);
 }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -350,7 +403,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 size_t balance_loss_ws_bytes(int64_t N, int32_t E, int32_t S) {
-  const size_t rows = static_cast<size_t>(loss_plan(N).chunks) + S;
+  const size_t rows = static_cast<size_t>(loss_plan(N, E).chunks) + S;
   return round256(rows * E * sizeof(float)) + rows * sizeof(double);
 }
 
@@ -358,7 +411,7 @@ cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_
                                 int32_t K, int32_t S, int score, double lambda, const float* grad_loss,
                                 int accumulate, float* loss, int32_t* counts, float* prob, float* gz, void* ws,
                                 cudaStream_t s) {
-  const LossPlan lp = loss_plan(N);
+  const LossPlan lp = loss_plan(N, E);
   LossParams p{};
   p.z = z;
   p.counts = counts;
@@ -387,7 +440,7 @@ cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_
 cudaError_t launch_balance_loss_grad(const float* z, const int32_t* counts, const int64_t* seq, int64_t N,
                                      int32_t E, int32_t K, int32_t S, int score, double lambda,
                                      const float* grad_loss, int accumulate, float* gz, cudaStream_t s) {
-  const LossPlan lp = loss_plan(N);
+  const LossPlan lp = loss_plan(N, E);
   LossParams p{};
   p.z = z;
   p.counts = counts;
