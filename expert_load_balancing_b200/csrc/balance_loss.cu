@@ -169,12 +169,131 @@ struct LossBlocks {
   static constexpr int kPerSm = V <= 3 ? 4 : 2;
 };
 
+// Rows [lo, hi) of sequence s, which is rows [b, e_), with its counts: writes
+// their gradient, and leaves the warps' shares of P and of sum dot in psum and
+// dsum (all threads of the block; ends with a barrier if kProb).
+template <int L, int V, bool kSoftmax, bool kProb, bool kGrad>
+__device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* counts, int s, int64_t b, int64_t e_,
+                                          int64_t lo, int64_t hi, float* psum, double* dsum) {
+  constexpr int kRows = 32 / L;          // rows of a warp at once
+  const int lane = threadIdx.x & (L - 1), group = (threadIdx.x & 31) / L, warp = threadIdx.x >> 5;
+  const int E4 = p.E >> 2;
+  // f - 1 = (E c - K T) / (K T), the numerator an integer: exact where loads are even
+  const int64_t slots = (e_ - b) * p.K;
+  const float per_slot = __fdiv_rn(1.0f, static_cast<float>(slots));
+  float fr[4 * V], acc[4 * V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c4 = lane + L * j;
+    int4 c = make_int4(0, 0, 0, 0);
+    if (c4 < E4) c = reinterpret_cast<const int4*>(counts)[c4];
+    fr[4 * j + 0] = static_cast<float>(static_cast<int64_t>(c.x) * p.E - slots) * per_slot;
+    fr[4 * j + 1] = static_cast<float>(static_cast<int64_t>(c.y) * p.E - slots) * per_slot;
+    fr[4 * j + 2] = static_cast<float>(static_cast<int64_t>(c.z) * p.E - slots) * per_slot;
+    fr[4 * j + 3] = static_cast<float>(static_cast<int64_t>(c.w) * p.E - slots) * per_slot;
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * V; ++i) acc[i] = 0.0f;
+  float gscale = 0.0f;
+  if constexpr (kGrad)
+    gscale = __fdiv_rn(static_cast<float>(p.lambda) * (p.grad_loss ? p.grad_loss[s] : 1.0f), static_cast<float>(e_ - b));
+  double dot_sum = 0.0;
+  for (int64_t base = lo + warp * kRows; base < hi; base += kRows * kLossWarps) {
+    const int64_t row = base + group;
+    const bool there = row < hi;
+    const float4* zr = reinterpret_cast<const float4*>(p.z) + row * E4;
+    float z[4 * V], u[4 * V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c4 = lane + L * j;
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (c4 < E4 && there) v = __ldcs(zr + c4);
+      z[4 * j] = v.x; z[4 * j + 1] = v.y; z[4 * j + 2] = v.z; z[4 * j + 3] = v.w;
+    }
+    float m = z[0];
+#pragma unroll
+    for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, z[i]);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool none = m == -INFINITY;               // a row behind the last one is such a row too
+    float sum = 0.0f, dot = 0.0f, ec = 1.0f;
+    if constexpr (kSoftmax) {
+      const float c = none ? 0.0f : m;
+#pragma unroll
+      for (int i = 0; i < 4 * V; ++i) z[i] = exp2_fast((z[i] - c) * kLog2e);
+    } else {
+      const float c = none ? 0.0f : fminf(m, 0.0f);
+      ec = exp2_fast(c * kLog2e);
+#pragma unroll
+      for (int i = 0; i < 4 * V; ++i) {
+        u[i] = exp2_fast((c - z[i]) * kLog2e);
+        z[i] = rcp_fast(ec + u[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * V; ++i) {
+      sum += z[i];
+      dot = fmaf(fr[i], z[i], dot);
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    }
+    const float inv = none ? 0.0f : rcp_fast(sum);
+    dot = __fmul_rn(dot, inv);          // uncontracted: the same bits in every form of the pass
+    if constexpr (kProb) {
+      dot_sum += !there ? 0.0f : none ? -1.0f : dot;         // a row without p adds nothing to L
+#pragma unroll
+      for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
+    }
+    if constexpr (kGrad) {
+      const float k = gscale * inv;
+      float4* gr = reinterpret_cast<float4*>(p.gz) + row * E4;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c4 = lane + L * j;
+        float o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int x = 4 * j + i;
+          o[i] = k * z[x] * (fr[x] - dot);
+          if constexpr (!kSoftmax) o[i] *= u[x] < ec ? z[x] * u[x] : fmaf(-z[x], ec, 1.0f);
+        }
+        if (c4 < E4 && there) {
+          if (p.accumulate) {
+            const float4 old = gr[c4];
+            o[0] += old.x; o[1] += old.y; o[2] += old.z; o[3] += old.w;
+          }
+          __stcs(gr + c4, make_float4(o[0], o[1], o[2], o[3]));
+        }
+      }
+    }
+  }
+  if constexpr (kProb) {
+    // the warp's rows at once, in a fixed order
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 4 * V; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+      dot_sum += __shfl_xor_sync(0xffffffffu, dot_sum, o);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c4 = lane + L * j;
+      if (c4 < E4 && group == 0)
+        reinterpret_cast<float4*>(psum + warp * kMaxE)[c4] =
+            make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+    }
+    if (lane == 0 && group == 0) dsum[warp] = dot_sum;
+    __syncthreads();
+  }
+}
+
 template <int L, int V, bool kSoftmax, bool kProb, bool kGrad>
 __global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_loss_kernel(const LossParams p) {
   __shared__ float psum[kProb ? kLossWarps * kMaxE : 1];
   __shared__ double dsum[kLossWarps];
-  constexpr int kRows = 32 / L;          // rows of a warp at once
-  const int lane = threadIdx.x & (L - 1), group = (threadIdx.x & 31) / L, warp = threadIdx.x >> 5;
   const int E4 = p.E >> 2;
   __shared__ int64_t seq_s[kSeqCache];
   const int64_t r0 = blockIdx.x * p.chunk;
@@ -197,116 +316,9 @@ __global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_l
     if (b >= r1) break;
     const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
     if (lo >= hi) continue;
-    // f - 1 = (E c - K T) / (K T), the numerator an integer: exact where loads are even
-    const int64_t slots = (e_ - b) * p.K;
-    const float per_slot = __fdiv_rn(1.0f, static_cast<float>(slots));
-    float fr[4 * V], acc[4 * V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c4 = lane + L * j;
-      int4 c = make_int4(0, 0, 0, 0);
-      if (c4 < E4) c = reinterpret_cast<const int4*>(p.counts)[static_cast<int64_t>(s) * E4 + c4];
-      fr[4 * j + 0] = static_cast<float>(static_cast<int64_t>(c.x) * p.E - slots) * per_slot;
-      fr[4 * j + 1] = static_cast<float>(static_cast<int64_t>(c.y) * p.E - slots) * per_slot;
-      fr[4 * j + 2] = static_cast<float>(static_cast<int64_t>(c.z) * p.E - slots) * per_slot;
-      fr[4 * j + 3] = static_cast<float>(static_cast<int64_t>(c.w) * p.E - slots) * per_slot;
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * V; ++i) acc[i] = 0.0f;
-    float gscale = 0.0f;
-    if constexpr (kGrad)
-      gscale = __fdiv_rn(static_cast<float>(p.lambda) * (p.grad_loss ? p.grad_loss[s] : 1.0f), static_cast<float>(e_ - b));
-    double dot_sum = 0.0;
-    for (int64_t base = lo + warp * kRows; base < hi; base += kRows * kLossWarps) {
-      const int64_t row = base + group;
-      const bool there = row < hi;
-      const float4* zr = reinterpret_cast<const float4*>(p.z) + row * E4;
-      float z[4 * V], u[4 * V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int c4 = lane + L * j;
-        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (c4 < E4 && there) v = __ldcs(zr + c4);
-        z[4 * j] = v.x; z[4 * j + 1] = v.y; z[4 * j + 2] = v.z; z[4 * j + 3] = v.w;
-      }
-      float m = z[0];
-#pragma unroll
-      for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, z[i]);
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const bool none = m == -INFINITY;               // a row behind the last one is such a row too
-      float sum = 0.0f, dot = 0.0f, ec = 1.0f;
-      if constexpr (kSoftmax) {
-        const float c = none ? 0.0f : m;
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) z[i] = exp2_fast((z[i] - c) * kLog2e);
-      } else {
-        const float c = none ? 0.0f : fminf(m, 0.0f);
-        ec = exp2_fast(c * kLog2e);
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) {
-          u[i] = exp2_fast((c - z[i]) * kLog2e);
-          z[i] = rcp_fast(ec + u[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4 * V; ++i) {
-        sum += z[i];
-        dot = fmaf(fr[i], z[i], dot);
-      }
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      }
-      const float inv = none ? 0.0f : rcp_fast(sum);
-      dot = __fmul_rn(dot, inv);          // uncontracted: the same bits in every form of the pass
-      if constexpr (kProb) {
-        dot_sum += !there ? 0.0f : none ? -1.0f : dot;         // a row without p adds nothing to L
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
-      }
-      if constexpr (kGrad) {
-        const float k = gscale * inv;
-        float4* gr = reinterpret_cast<float4*>(p.gz) + row * E4;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int c4 = lane + L * j;
-          float o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int x = 4 * j + i;
-            o[i] = k * z[x] * (fr[x] - dot);
-            if constexpr (!kSoftmax) o[i] *= u[x] < ec ? z[x] * u[x] : fmaf(-z[x], ec, 1.0f);
-          }
-          if (c4 < E4 && there) {
-            if (p.accumulate) {
-              const float4 old = gr[c4];
-              o[0] += old.x; o[1] += old.y; o[2] += old.z; o[3] += old.w;
-            }
-            __stcs(gr + c4, make_float4(o[0], o[1], o[2], o[3]));
-          }
-        }
-      }
-    }
+    loss_rows<L, V, kSoftmax, kProb, kGrad>(p, p.counts + static_cast<int64_t>(s) * p.E, s, b, e_, lo, hi, psum, dsum);
     if constexpr (kProb) {
       const int64_t slot = blockIdx.x + s;
-      // the warp's rows at once, in a fixed order
-#pragma unroll
-      for (int o = L; o < 32; o <<= 1) {
-#pragma unroll
-        for (int i = 0; i < 4 * V; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-        dot_sum += __shfl_xor_sync(0xffffffffu, dot_sum, o);
-      }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int c4 = lane + L * j;
-        if (c4 < E4 && group == 0)
-          reinterpret_cast<float4*>(psum + warp * kMaxE)[c4] =
-              make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-      }
-      if (lane == 0 && group == 0) dsum[warp] = dot_sum;
-      __syncthreads();
       for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
         float t = 0.0f;
 #pragma unroll
@@ -365,6 +377,103 @@ __global__ void __launch_bounds__(32 * kFinishRows) balance_finish_kernel(const 
   }
 }
 
+// A small batch of one sequence: one launch, a cluster of eight blocks that
+// hold the counts and the shares of P in shared memory and read one another's.
+// The four launches of the other form cost 12 us whatever the size.
+constexpr int kClusterBlocks = 8;
+constexpr int64_t kSmallRows = 1024;
+
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ double remote_f64(const void* p, uint32_t rank) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int L, int V, bool kSoftmax, bool kGrad>
+__global__ void __launch_bounds__(kLossThreads) balance_small_kernel(const LossParams p, const int32_t* ids,
+                                                                     int32_t* counts_out, float* prob, float* loss) {
+  __shared__ float psum[kLossWarps * kMaxE];
+  __shared__ double dsum[kLossWarps];
+  __shared__ int32_t hist[kMaxE];
+  __shared__ __align__(16) int32_t counts[kMaxE];
+  __shared__ float share[kMaxE];
+  __shared__ double dots;
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  for (int e = threadIdx.x; e < p.E; e += kLossThreads) hist[e] = 0;
+  pdl_wait();
+  const Seqs q = p.q;
+  if (rank == 0 && threadIdx.x == 0 && q.seq && (q.seq[0] < 0 || q.seq[0] > q.seq[1] || q.seq[1] > q.N))
+    raise_status(kStatusBadInput);
+  const int64_t b = q.at(0), end = q.at(1), e_ = end > b ? end : b;
+  const int64_t r0 = rank * p.chunk, r1 = r0 + p.chunk < q.N ? r0 + p.chunk : q.N;
+  const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
+  __syncthreads();
+  for (int64_t j = lo * p.K + threadIdx.x; j < hi * p.K; j += kLossThreads) {
+    const int32_t e = ids[j];
+    if (e >= 0 && e < p.E) atomicAdd(&hist[e], 1);
+    else raise_status(kStatusBadInput);
+  }
+  cluster_barrier();
+  for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
+    int32_t c = 0;
+#pragma unroll
+    for (uint32_t r = 0; r < kClusterBlocks; ++r) c += static_cast<int32_t>(remote_u32(hist + e, r));
+    counts[e] = c;
+    if (rank == 0) counts_out[e] = c;
+  }
+  __syncthreads();
+  if constexpr (kGrad) {
+    if (!p.accumulate)
+      for (int64_t i = r0 * p.E + threadIdx.x; i < r1 * p.E; i += kLossThreads)
+        if (i < b * p.E || i >= e_ * p.E) p.gz[i] = 0.0f;
+  }
+  if (threadIdx.x < kLossWarps) dsum[threadIdx.x] = 0.0;
+  for (int i = threadIdx.x; i < kLossWarps * kMaxE; i += kLossThreads) psum[i] = 0.0f;
+  __syncthreads();
+  if (lo < hi) loss_rows<L, V, kSoftmax, true, kGrad>(p, counts, 0, b, e_, lo, hi, psum, dsum);
+  for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kLossWarps; ++w) t += psum[w * kMaxE + e];
+    share[e] = t;
+  }
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kLossWarps; ++w) t += dsum[w];
+    dots = t;
+  }
+  cluster_barrier();
+  const int64_t n = e_ - b;
+  for (int e = rank * kLossThreads + threadIdx.x; e < p.E; e += kClusterBlocks * kLossThreads) {
+    double t = 0.0;
+#pragma unroll
+    for (uint32_t r = 0; r < kClusterBlocks; ++r) t += __uint_as_float(remote_u32(share + e, r));
+    prob[e] = n ? static_cast<float>(t / static_cast<double>(n)) : 0.0f;
+  }
+  if (rank == kClusterBlocks - 1 && threadIdx.x == 0) {
+    double t = 0.0;
+#pragma unroll
+    for (uint32_t r = 0; r < kClusterBlocks; ++r) t += remote_f64(&dots, r);
+    loss[0] = n ? static_cast<float>(p.lambda * (1.0 + t / static_cast<double>(n))) : 0.0f;
+  }
+  cluster_barrier();                     // no block leaves while another reads its shared memory
+}
+
 struct LossPlan {
   int64_t chunk, chunks;
 };
@@ -380,22 +489,43 @@ LossPlan loss_plan(int64_t N, int32_t E) {
   return lp;
 }
 
-template <int L, int V, bool kProb, bool kGrad>
-cudaError_t launch_loss_pass(const LossParams& p, int score, int64_t chunks, cudaStream_t s) {
-  auto kern = score == KOLIBRI_SCORE_SOFTMAX ? balance_loss_kernel<L, V, true, kProb, kGrad>
-                                             : balance_loss_kernel<L, V, false, kProb, kGrad>;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(chunks)), dim3(kLossThreads), 0, s, dim3(0, 0, 0), p);
-}
+template <bool kProb, bool kGrad>
+struct LossPass {
+  int64_t chunks;
+  template <int L, int V>
+  cudaError_t run(const LossParams& p, int score, cudaStream_t s) const {
+    auto kern = score == KOLIBRI_SCORE_SOFTMAX ? balance_loss_kernel<L, V, true, kProb, kGrad>
+                                               : balance_loss_kernel<L, V, false, kProb, kGrad>;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(chunks)), dim3(kLossThreads), 0, s, dim3(0, 0, 0), p);
+  }
+};
+
+struct SmallPass {
+  const int32_t* ids;
+  int32_t* counts;
+  float* prob;
+  float* loss;
+  template <int L, int V, bool kSoftmax>
+  cudaError_t launch(const LossParams& p, cudaStream_t s) const {
+    auto kern = p.gz ? balance_small_kernel<L, V, kSoftmax, true> : balance_small_kernel<L, V, kSoftmax, false>;
+    return launch_pdl(kern, dim3(kClusterBlocks), dim3(kLossThreads), 0, s, dim3(kClusterBlocks, 1, 1), p, ids, counts,
+                      prob, loss);
+  }
+  template <int L, int V>
+  cudaError_t run(const LossParams& p, int score, cudaStream_t s) const {
+    return score == KOLIBRI_SCORE_SOFTMAX ? launch<L, V, true>(p, s) : launch<L, V, false>(p, s);
+  }
+};
 
 // The fewest lanes whose four float4s hold a row.
-template <bool kProb, bool kGrad>
-cudaError_t launch_loss_v(const LossParams& p, int score, int64_t chunks, cudaStream_t s) {
-  if (p.E <= 64) return launch_loss_pass<8, 2, kProb, kGrad>(p, score, chunks, s);
-  if (p.E <= 128) return launch_loss_pass<8, 4, kProb, kGrad>(p, score, chunks, s);
-  if (p.E <= 192) return launch_loss_pass<16, 3, kProb, kGrad>(p, score, chunks, s);
-  if (p.E <= 256) return launch_loss_pass<16, 4, kProb, kGrad>(p, score, chunks, s);
-  if (p.E <= 384) return launch_loss_pass<32, 3, kProb, kGrad>(p, score, chunks, s);
-  return launch_loss_pass<32, 4, kProb, kGrad>(p, score, chunks, s);
+template <typename Pass>
+cudaError_t launch_by_width(const Pass& pass, const LossParams& p, int score, cudaStream_t s) {
+  if (p.E <= 64) return pass.template run<8, 2>(p, score, s);
+  if (p.E <= 128) return pass.template run<8, 4>(p, score, s);
+  if (p.E <= 192) return pass.template run<16, 3>(p, score, s);
+  if (p.E <= 256) return pass.template run<16, 4>(p, score, s);
+  if (p.E <= 384) return pass.template run<32, 3>(p, score, s);
+  return pass.template run<32, 4>(p, score, s);
 }
 
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -426,12 +556,17 @@ cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_
   p.K = K;
   p.accumulate = accumulate;
   p.lambda = lambda;
+  if (S == 1 && N <= kSmallRows) {
+    p.chunk = (N + kClusterBlocks - 1) / kClusterBlocks;
+    return launch_by_width(SmallPass{ids, counts, prob, loss}, p, score, s);
+  }
   cudaError_t err = cudaMemsetAsync(counts, 0, sizeof(int32_t) * static_cast<size_t>(S) * E, s);
   if (err != cudaSuccess) return err;
   seq_count_kernel<<<static_cast<unsigned>(lp.chunks), kLossThreads, 0, s>>>(ids, p.q, E, K, lp.chunk, counts);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  err = gz ? launch_loss_v<true, true>(p, score, lp.chunks, s) : launch_loss_v<true, false>(p, score, lp.chunks, s);
+  err = gz ? launch_by_width(LossPass<true, true>{lp.chunks}, p, score, s)
+           : launch_by_width(LossPass<true, false>{lp.chunks}, p, score, s);
   if (err != cudaSuccess) return err;
   return launch_pdl(balance_finish_kernel, dim3(static_cast<unsigned>((E + 31) / 32) * S), dim3(32, kFinishRows), 0, s, dim3(0, 0, 0), p, prob,
                     loss);
@@ -452,7 +587,7 @@ cudaError_t launch_balance_loss_grad(const float* z, const int32_t* counts, cons
   p.K = K;
   p.accumulate = accumulate;
   p.lambda = lambda;
-  return launch_loss_v<false, true>(p, score, lp.chunks, s);
+  return launch_by_width(LossPass<false, true>{lp.chunks}, p, score, s);
 }
 
 KOLIBRI_DEFINE_STATUS_TAKE(status_take_balance_loss)

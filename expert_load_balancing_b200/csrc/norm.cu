@@ -37,24 +37,42 @@ struct Vec8 {
   float v[kVec];
 };
 
+// Eight elements as they lie in memory: 16 bytes of bf16, 32 of fp32.
 template <typename T>
-__device__ __forceinline__ Vec8 load8(const void* p, int64_t vec) {
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const void* p, int64_t vec) {
+  Raw8<T> r;
+  const uint4* q = reinterpret_cast<const uint4*>(p) + vec * (sizeof(T) / 2);
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = q[i];
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ Vec8 widen(const Raw8<T>& r) {
   Vec8 o;
   if constexpr (sizeof(T) == 2) {
-    const uint4 u = reinterpret_cast<const uint4*>(p)[vec];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       o.v[2 * i] = __uint_as_float(w[i] << 16);
       o.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else {
-    const float4* q = reinterpret_cast<const float4*>(p) + 2 * vec;
-    const float4 a = q[0], b = q[1];
-    o.v[0] = a.x; o.v[1] = a.y; o.v[2] = a.z; o.v[3] = a.w;
-    o.v[4] = b.x; o.v[5] = b.y; o.v[6] = b.z; o.v[7] = b.w;
+    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o.v[i] = __uint_as_float(w[i]);
   }
   return o;
+}
+
+template <typename T>
+__device__ __forceinline__ Vec8 load8(const void* p, int64_t vec) {
+  return widen<T>(load_raw<T>(p, vec));
 }
 
 template <typename T>
@@ -118,77 +136,77 @@ struct NormParams {
 
 struct NoRes {};
 
-// A block per row and step; thread t holds the vecs t, t + T, ... of the row.
-// T is a multiple of 32, so a scale group is 16 neighbouring lanes.
+// A block per row; thread t holds the vecs t, t + T, ... of the row.  T is a
+// multiple of 32, so a scale group is 16 neighbouring lanes.  Blocks that stay
+// and walk over rows, the weight in registers, read no faster and left some SMs
+// a row more than others (65,536 rows of 2048: 270 us, a block per row 238).
 template <typename XT, typename RT, int C>
 __global__ void __launch_bounds__(C == 1 ? 512 : kMaxNormThreads) rms_norm_kernel(const NormParams p) {
   constexpr bool kRes = !std::is_same<RT, NoRes>::value;
-  __shared__ float buf[2][kMaxNormWarps];
+  __shared__ float buf[kMaxNormWarps];
   const int T = blockDim.x, warps = T >> 5;
+  const int64_t row = blockIdx.x;
+  const int64_t base = row * p.nvec;
+  Vec8 h[C];
   Vec8 g[C];
+  float ss[1] = {0.0f};
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int v = threadIdx.x + c * T;
+    if (v < p.nvec) {
+      h[c] = load8<XT>(p.x, base + v);
+      if constexpr (kRes) {
+        const Vec8 r = load8<RT>(p.res, base + v);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) h[c].v[i] += r.v[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) h[c].v[i] = 0.0f;
+    }
+  }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int v = threadIdx.x + c * T;
     if (v < p.nvec) g[c] = load_weight(p.g, p.g_f32, v);
   }
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
-    const int64_t base = row * p.nvec;
-    Vec8 h[C];
-    float ss[1] = {0.0f};
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
+  for (int c = 0; c < C; ++c) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) ss[0] = fmaf(h[c].v[i], h[c].v[i], ss[0]);
+    if constexpr (kRes) {
       const int v = threadIdx.x + c * T;
-      if (v < p.nvec) {
-        h[c] = load8<XT>(p.x, base + v);
-        if constexpr (kRes) {
-          const Vec8 r = load8<RT>(p.res, base + v);
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) h[c].v[i] += r.v[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) h[c].v[i] = 0.0f;
-      }
+      if (p.res_out && v < p.nvec) store8<RT>(p.res_out, base + v, h[c]);
     }
+  }
+  block_sums<1>(ss, buf, warps);
+  const float r = rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
+  for (int c = 0; c < C; ++c) {
+    const int v = threadIdx.x + c * T;
+    const bool in = v < p.nvec;
+    Vec8 y;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) ss[0] = fmaf(h[c].v[i], h[c].v[i], ss[0]);
-      if constexpr (kRes) {
-        const int v = threadIdx.x + c * T;
-        if (p.res_out && v < p.nvec) store8<RT>(p.res_out, base + v, h[c]);
+    for (int i = 0; i < kVec; ++i) y.v[i] = in ? h[c].v[i] * r * g[c].v[i] : 0.0f;
+    if (p.y && in) store8<__nv_bfloat16>(p.y, base + v, y);
+    if (p.y8) {
+      float a = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) a = fmaxf(a, fabsf(y.v[i]));
+#pragma unroll
+      for (int o = kGroupVecs / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      a = fmaxf(a, kAmaxMin);
+      const float q = __fdiv_rn(kE4m3Max, a);
+      uint32_t w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y.v[4 * i] * q, y.v[4 * i + 1] * q), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y.v[4 * i + 2] * q, y.v[4 * i + 3] * q), __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | (hi << 16);
       }
-    }
-    block_sums<1>(ss, buf[flip], warps);
-    const float r = rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int v = threadIdx.x + c * T;
-      const bool in = v < p.nvec;
-      Vec8 y;
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) y.v[i] = in ? h[c].v[i] * r * g[c].v[i] : 0.0f;
-      if (p.y && in) store8<__nv_bfloat16>(p.y, base + v, y);
-      if (p.y8) {
-        float a = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) a = fmaxf(a, fabsf(y.v[i]));
-#pragma unroll
-        for (int o = kGroupVecs / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        a = fmaxf(a, kAmaxMin);
-        const float q = __fdiv_rn(kE4m3Max, a);
-        uint32_t w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y.v[4 * i] * q, y.v[4 * i + 1] * q), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y.v[4 * i + 2] * q, y.v[4 * i + 3] * q), __NV_SATFINITE, __NV_E4M3);
-          w[i] = lo | (hi << 16);
-        }
-        if (in) {
-          reinterpret_cast<uint2*>(p.y8)[base + v] = make_uint2(w[0], w[1]);
-          if (v % kGroupVecs == 0) p.scales[row * p.groups + v / kGroupVecs] = __fdiv_rn(a, kE4m3Max);
-        }
+      if (in) {
+        reinterpret_cast<uint2*>(p.y8)[base + v] = make_uint2(w[0], w[1]);
+        if (v % kGroupVecs == 0) p.scales[row * p.groups + v / kGroupVecs] = __fdiv_rn(a, kE4m3Max);
       }
     }
   }
@@ -217,8 +235,14 @@ struct NormGradParams {
   float inv_d, eps;
 };
 
-template <typename GT, typename HT, int C>
-__global__ void __launch_bounds__(C == 1 ? 512 : kMaxNormThreads) rms_norm_grad_kernel(const NormGradParams p) {
+//
+// The next row's inputs are loaded before this row is reduced, and both rows
+// stay as they lie in memory until they are used: with each row's loads behind
+// the last one's barrier 16,384 rows of 2560 (bf16, gres) took 101 us, with both
+// rows held in fp32 89, so 56.5.
+template <typename GT, typename HT, int C, bool kRes, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1) rms_norm_grad_kernel(const NormGradParams p) {
+  constexpr bool kAhead = kThreads <= 512;      // rows above 8192 columns: no registers for a second one
   __shared__ float buf[2][2 * kMaxNormWarps];
   const int T = blockDim.x, warps = T >> 5;
   Vec8 g[C], gg[C];
@@ -229,29 +253,47 @@ __global__ void __launch_bounds__(C == 1 ? 512 : kMaxNormThreads) rms_norm_grad_
     for (int i = 0; i < kVec; ++i) g[c].v[i] = gg[c].v[i] = 0.0f;
     if (v < p.nvec) g[c] = load_weight(p.g, p.g_f32, v);
   }
-  int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
-    const int64_t base = row * p.nvec;
-    Vec8 h[C], t[C];
-    float s[2] = {0.0f, 0.0f};
+  Raw8<HT> h[C], a[kRes ? C : 1], nh[C], na[kRes ? C : 1];
+  Raw8<GT> t[C], nt[C];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int v = threadIdx.x + c * T;
       if (v < p.nvec) {
-        h[c] = load8<HT>(p.h, base + v);
-        t[c] = load8<GT>(p.gy, base + v);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) h[c].v[i] = t[c].v[i] = 0.0f;
+        nh[c] = load_raw<HT>(p.h, row * p.nvec + v);
+        nt[c] = load_raw<GT>(p.gy, row * p.nvec + v);
+        if constexpr (kRes) na[c] = load_raw<HT>(p.gres, row * p.nvec + v);
       }
     }
+  };
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    nh[c] = Raw8<HT>{};
+    nt[c] = Raw8<GT>{};
+    if constexpr (kRes) na[c] = Raw8<HT>{};
+  }
+  if (kAhead && blockIdx.x < p.N) fetch(blockIdx.x);
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
+    const int64_t base = row * p.nvec;
+    float s[2] = {0.0f, 0.0f};
+    if constexpr (!kAhead) fetch(row);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      h[c] = nh[c];
+      t[c] = nt[c];
+      if constexpr (kRes) a[c] = na[c];
+    }
+    if (kAhead && row + gridDim.x < p.N) fetch(row + gridDim.x);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const Vec8 hv = widen<HT>(h[c]), tv = widen<GT>(t[c]);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        s[0] = fmaf(h[c].v[i], h[c].v[i], s[0]);
-        s[1] = fmaf(t[c].v[i] * g[c].v[i], h[c].v[i], s[1]);
+        s[0] = fmaf(hv.v[i], hv.v[i], s[0]);
+        s[1] = fmaf(tv.v[i] * g[c].v[i], hv.v[i], s[1]);
       }
+    }
     block_sums<2>(s, buf[flip], warps);
     const float r = rsqrtf(fmaf(s[0], p.inv_d, p.eps));
     const float k = r * r * r * (s[1] * p.inv_d);
@@ -259,16 +301,17 @@ __global__ void __launch_bounds__(C == 1 ? 512 : kMaxNormThreads) rms_norm_grad_
     for (int c = 0; c < C; ++c) {
       const int v = threadIdx.x + c * T;
       if (v < p.nvec) {
+        const Vec8 hv = widen<HT>(h[c]), tv = widen<GT>(t[c]);
         Vec8 o;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-          gg[c].v[i] = fmaf(t[c].v[i], h[c].v[i] * r, gg[c].v[i]);
-          o.v[i] = fmaf(t[c].v[i] * g[c].v[i], r, -h[c].v[i] * k);
+          gg[c].v[i] = fmaf(tv.v[i], hv.v[i] * r, gg[c].v[i]);
+          o.v[i] = fmaf(tv.v[i] * g[c].v[i], r, -hv.v[i] * k);
         }
-        if (p.gres) {
-          const Vec8 a = load8<HT>(p.gres, base + v);
+        if constexpr (kRes) {
+          const Vec8 av = widen<HT>(a[c]);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) o.v[i] += a.v[i];
+          for (int i = 0; i < kVec; ++i) o.v[i] += av.v[i];
         }
         store8<HT>(p.gx, base + v, o);
       }
@@ -306,14 +349,16 @@ __global__ void __launch_bounds__(1024) norm_weight_sum_kernel(const float* part
 struct RowPlan {
   int c, threads;
 };
-RowPlan row_plan(int nvec, int64_t N) {
+// One vec each while a block's threads suffice: 16,384 rows of 2560 take the
+// norm 63.5 us at one, 70 at two.  The gradient keeps a row and the next one in
+// flight and rather has two (56.5 us, 62 at one) unless there are few rows.
+RowPlan row_plan(int nvec, int64_t N, bool grad) {
   RowPlan rp;
-  rp.c = nvec > 512 || (nvec > 64 && N > 1024) ? 2 : 1;
+  rp.c = nvec > 512 || (grad && nvec > 64 && N > 1024) ? 2 : 1;
   rp.threads = ((nvec + rp.c - 1) / rp.c + 31) / 32 * 32;
   return rp;
 }
 
-constexpr int kNormBlocksPerSm = 12;
 constexpr int kNormGradBlocksPerSm = 6;
 
 unsigned row_grid(int64_t N, int threads, int per_sm) {
@@ -324,8 +369,8 @@ unsigned row_grid(int64_t N, int threads, int per_sm) {
 
 template <typename XT, typename RT>
 void launch_norm_c(const NormParams& p, cudaStream_t s) {
-  const RowPlan rp = row_plan(p.nvec, p.N);
-  const unsigned grid = row_grid(p.N, rp.threads, kNormBlocksPerSm);
+  const RowPlan rp = row_plan(p.nvec, p.N, false);
+  const unsigned grid = static_cast<unsigned>(p.N);
   if (rp.c == 1) rms_norm_kernel<XT, RT, 1><<<grid, rp.threads, 0, s>>>(p);
   else rms_norm_kernel<XT, RT, 2><<<grid, rp.threads, 0, s>>>(p);
 }
@@ -337,10 +382,28 @@ void launch_norm_x(const NormParams& p, int res_type, cudaStream_t s) {
   else launch_norm_c<XT, float>(p, s);
 }
 
+// One wave: as many blocks as are resident at once, at most `grid`.
+template <typename GT, typename HT, int C, bool kRes, int kThreads>
+unsigned launch_norm_grad_t(const NormGradParams& p, int threads, unsigned grid, cudaStream_t s) {
+  static int per_sm[kMaxNormThreads / 32 + 1];
+  auto kern = rms_norm_grad_kernel<GT, HT, C, kRes, kThreads>;
+  int& n = per_sm[threads / 32];
+  if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess || n < 1)) n = 1;
+  const unsigned most = static_cast<unsigned>(n * device_sm_count());
+  if (grid > most) grid = most;
+  kern<<<grid, threads, 0, s>>>(p);
+  return grid;
+}
+template <typename GT, typename HT, bool kRes>
+unsigned launch_norm_grad_c(const NormGradParams& p, const RowPlan& rp, unsigned grid, cudaStream_t s) {
+  if (rp.c == 1) return launch_norm_grad_t<GT, HT, 1, kRes, 512>(p, rp.threads, grid, s);
+  if (rp.threads <= 256) return launch_norm_grad_t<GT, HT, 2, kRes, 256>(p, rp.threads, grid, s);
+  if (rp.threads <= 512) return launch_norm_grad_t<GT, HT, 2, kRes, 512>(p, rp.threads, grid, s);
+  return launch_norm_grad_t<GT, HT, 2, kRes, kMaxNormThreads>(p, rp.threads, grid, s);
+}
 template <typename GT, typename HT>
-void launch_norm_grad_c(const NormGradParams& p, const RowPlan& rp, unsigned grid, cudaStream_t s) {
-  if (rp.c == 1) rms_norm_grad_kernel<GT, HT, 1><<<grid, rp.threads, 0, s>>>(p);
-  else rms_norm_grad_kernel<GT, HT, 2><<<grid, rp.threads, 0, s>>>(p);
+unsigned launch_norm_grad_r(const NormGradParams& p, const RowPlan& rp, unsigned grid, cudaStream_t s) {
+  return p.gres ? launch_norm_grad_c<GT, HT, true>(p, rp, grid, s) : launch_norm_grad_c<GT, HT, false>(p, rp, grid, s);
 }
 
 }  // namespace
@@ -368,7 +431,7 @@ cudaError_t launch_rms_norm(const void* x, int x_type, const void* res, int res_
 }
 
 size_t rms_norm_grad_ws_bytes(int64_t N, int32_t d) {
-  const RowPlan rp = row_plan(d / kVec, N);
+  const RowPlan rp = row_plan(d / kVec, N, true);
   return sizeof(float) * static_cast<size_t>(row_grid(N, rp.threads, kNormGradBlocksPerSm)) * d;
 }
 
@@ -388,14 +451,14 @@ cudaError_t launch_rms_norm_grad(const void* gy, int gy_type, const void* h, int
   p.g_f32 = weight_type == KOLIBRI_TYPE_F32;
   p.inv_d = 1.0f / static_cast<float>(d);
   p.eps = eps;
-  const RowPlan rp = row_plan(p.nvec, N);
-  const unsigned grid = row_grid(N, rp.threads, kNormGradBlocksPerSm);
+  const RowPlan rp = row_plan(p.nvec, N, true);
+  unsigned grid = row_grid(N, rp.threads, kNormGradBlocksPerSm);      // as the workspace was sized, at most
   if (gy_type == KOLIBRI_TYPE_BF16) {
-    if (h_type == KOLIBRI_TYPE_BF16) launch_norm_grad_c<__nv_bfloat16, __nv_bfloat16>(p, rp, grid, s);
-    else launch_norm_grad_c<__nv_bfloat16, float>(p, rp, grid, s);
+    if (h_type == KOLIBRI_TYPE_BF16) grid = launch_norm_grad_r<__nv_bfloat16, __nv_bfloat16>(p, rp, grid, s);
+    else grid = launch_norm_grad_r<__nv_bfloat16, float>(p, rp, grid, s);
   } else {
-    if (h_type == KOLIBRI_TYPE_BF16) launch_norm_grad_c<float, __nv_bfloat16>(p, rp, grid, s);
-    else launch_norm_grad_c<float, float>(p, rp, grid, s);
+    if (h_type == KOLIBRI_TYPE_BF16) grid = launch_norm_grad_r<float, __nv_bfloat16>(p, rp, grid, s);
+    else grid = launch_norm_grad_r<float, float>(p, rp, grid, s);
   }
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || !gweight) return err;

@@ -82,7 +82,7 @@ def _inputs(N, E, K, cut, seed, spread=1.5):
 
 
 CASES = [
-    (1, 4, 1, [0, 1]), (1, 384, 6, [0, 1]), (2, 8, 3, [0, 1, 2]), (5, 132, 8, [0, 0, 5, 5]), (7, 128, 8, [0, 7]),
+    (1, 4, 1, [0, 1]), (1024, 384, 6, [0, 1024]), (1024, 512, 3, [100, 900]), (1025, 384, 6, [0, 1025]), (1000, 64, 8, [0, 0]), (513, 200, 2, [7, 513]), (900, 128, 4, [0, 3]), (1, 384, 6, [0, 1]), (2, 8, 3, [0, 1, 2]), (5, 132, 8, [0, 0, 5, 5]), (7, 128, 8, [0, 7]),
     (256, 384, 6, [0, 256]), (257, 260, 2, [0, 100, 100, 257]), (1000, 512, 16, [0, 1, 2, 3, 500, 1000]),
     (4096, 384, 6, [0, 4096]), (5003, 128, 8, [0, 17, 4000, 4000, 4001, 5003]), (700, 64, 1, list(range(0, 701))),
     (6000, 12, 5, [0, 2999, 6000]), (40001, 256, 4, [0, 12345, 40001]),
@@ -94,7 +94,7 @@ CASES = [
 def test_loss_counts_and_gradient(N, E, K, cut, score):
     z, ids, seq, up = _inputs(N, E, K, cut, N + E)
     want = _plain(z, ids, 1e-3, cut, score, up)
-    one = len(cut) == 2
+    one = cut == [0, N]
     got = B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq, score=score, grad_loss=up, want_gz=True)
     _check(got, want)
     # forward alone, the gradient alone, and again: the same bits
@@ -172,7 +172,7 @@ def test_bad_ids_and_offsets_are_reported():
     _, counts, _, _ = B.kolibri_balance_loss(z, twice, 1e-3)
     assert int(counts.sum()) == N * K
     assert torch.equal(counts[0].long(), torch.bincount(twice.reshape(-1).long(), minlength=E))
-    for cut in ([0, 200, 100], [-5, 100, N], [0, 100, N + 1], [300, 0, 300]):
+    for cut in ([0, 200, 100], [-5, 100, N], [0, 100, N + 1], [300, 0, 300], [0, N + 1], [200, 100], [-1, N]):
         B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=torch.tensor(cut, device="cuda"), want_gz=True)
         assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE
     check_status()
