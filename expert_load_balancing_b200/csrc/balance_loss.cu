@@ -133,21 +133,10 @@ struct LossParams {
   double lambda;
 };
 
-// 2^x and 1 / x by the hardware's approximations, subnormal results flushed:
-// 2^-22 relative each, and the product with log2 e adds 2^-24 |z - c|; far below
-// the 2^-24 sqrt(T) of the sums they enter.  (c is subtracted first: folded into
-// one multiply-add it would cost 2^-24 of |z| for logits far from zero.)
-constexpr float kLog2e = 1.44269504088896340736f;
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+// The product with log2 e adds 2^-24 |z - c| to exp2_fast's error; all far below
+// the 2^-24 sqrt(T) of the sums the scores enter.  (c is subtracted first:
+// folded into one multiply-add it would cost 2^-24 of |z| for logits far from
+// zero.)
 
 // L lanes per row (8, 16 or 32): lane l of them holds the float4s l, l + L, ...
 // (V of them) of the row's E logits.  Narrow rows share a warp, so that a row's
