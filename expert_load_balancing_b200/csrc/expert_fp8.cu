@@ -32,6 +32,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "launch.h"
 #include "gemm_pair.cuh"
 #include "pdl.cuh"
@@ -475,8 +477,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       const int srow = (place.x & 3) + r;
       const float* const w0 = ws_s[t][kGateUp ? 0 : half];
       float2 acc[4][16];
-      for (int kb = 0; kb < p.k_blocks; ++kb) {
-        if (!mbar_wait(bars.done(stage), phase)) { ok = false; break; }
+      // one k block; the first sets the sums (a choice inside one loop body costs both instructions)
+      auto add = [&](int kb, auto first) -> bool {
+        if (!mbar_wait(bars.done(stage), phase)) return false;
         tc_fence_after();
         auto release = [&]() {           // the buffer's columns of this warp are in registers
           tc_fence_before();
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             const uint64_t f = c < 2 ? f0 : f1;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              if (kb == 0) acc[c][i] = mul2(v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
+              if constexpr (decltype(first)::value) acc[c][i] = mul2(v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
               else fma2(acc[c][i], v[c & 1][2 * i], v[c & 1][2 * i + 1], f);
             }
             if (c < 3) tmem_wait_ld32(v[(c + 1) & 1]);
@@ -512,7 +515,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           stage = 0;
           phase ^= 1u;
         }
-      }
+        return true;
+      };
+      ok = add(0, std::true_type{});
+      for (int kb = 1; kb < p.k_blocks && ok; ++kb) ok = add(kb, std::false_type{});
       if (!ok) break;
       if (lane == 0) mbar_arrive(bars.told(t));
       t ^= 1;
