@@ -338,6 +338,13 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(bars.holder()) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // Rows that no tile of the block has stay zero: what stood there would be multiplied all the same, at a power
+  // that lowers the GPU's clock (64 tokens in 384 experts: 179 -> 172 us, 195 -> 187 under the power cap).
+  for (int i = threadIdx.x; i < C::kStages * static_cast<int>(kABytes / 16); i += kF8Threads) {
+    const uint32_t at = ring + kF8Stage * (i / (kABytes / 16)) + 16u * (i % (kABytes / 16));
+    *reinterpret_cast<uint4*>(smem_raw + (at - raw)) = make_uint4(0, 0, 0, 0);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   pdl_wait();
   f8_tile_prefix(p, G, mt_s, off_s, warp_tot);
   tc_fence_before();

@@ -150,6 +150,9 @@ CASES = [
     (1500, 256, 512, 32, 16, False, False), (333, 2048, 512, 128, 8, False, False), (2000, 512, 128, 512, 6, True, False),
     (3001, 768, 256, 5, 2, True, False),
     (1, 8192, 128, 4, 2, True, False), (1, 256, 8192, 4, 1, True, False), (260, 4352, 128, 4, 1, False, False), (150, 256, 4224, 4, 1, True, False),
+    # a few rows per expert, some of them with many
+    (64, 2560, 512, 384, 6, True, False), (100, 512, 256, 128, 4, True, True), (65, 256, 128, 512, 1, True, False),
+    (500, 768, 384, 64, 1, True, False), (12, 8192, 128, 64, 8, False, False), (12, 256, 8192, 64, 8, True, False),
     # several tiles per block: every barrier goes round many times
     (20000, 256, 512, 6, 2, True, False), (4000, 2048, 256, 4, 2, False, False), (9000, 1024, 384, 3, 1, True, True),
 ]
@@ -217,16 +220,17 @@ def test_gates_of_zero_and_a_shared_expert_alone():
 
 def test_bad_entries_are_reported():
     """Out-of-range perm and inv entries and broken offsets set the status word; every access stays in the arrays."""
-    for key, bad in (("perm", -1), ("perm", 1 << 30), ("inv", -7), ("inv", 300 * 2)):
-        c = _case(300, 256, 128, 8, 2, True, 5)
-        c[key][13] = bad
-        _call(c)
-        assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, (key, bad)
-    for i, v in ((0, 1), (8, 599), (8, 1 << 40), (4, -1), (4, 1 << 35)):
-        c = _case(300, 256, 128, 8, 2, False, 5)
-        c["off"][i] = v
-        _call(c)
-        assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, (i, v)
+    for E in (8, 128):
+        for key, bad in (("perm", -1), ("perm", 1 << 30), ("inv", -7), ("inv", 300 * 2)):
+            c = _case(300, 256, 128, E, 2, True, 5)
+            c[key][13] = bad
+            _call(c)
+            assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, (E, key, bad)
+        for i, v in ((0, 1), (E, 599), (E, 1 << 40), (4, -1), (4, 1 << 35)):
+            c = _case(300, 256, 128, E, 2, False, 5)
+            c["off"][i] = v
+            _call(c)
+            assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, (E, i, v)
     check_status()
 
 
@@ -272,7 +276,7 @@ def test_refusals():
 
 
 def test_other_stream_and_graph():
-    for N in (1, 400):
+    for N in (1, 30, 400):
         c = _case(N, 1280, 256, 16, 4, True, 7)
         want = _call(c)
         torch.cuda.synchronize()
