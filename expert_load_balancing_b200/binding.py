@@ -712,6 +712,14 @@ def _raw_stream(stream, index):
     return _current_raw(index) if _current_raw else torch.cuda.current_stream(index).cuda_stream
 
 
+def _made(stream, t):
+    """A tensor allocated by the call itself (on the current stream): with a stream given, its memory is not handed out
+    again before that stream is through with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _type_of(t, name):
     code = _TYPE.get(t.dtype)
     if code is None:
@@ -736,14 +744,14 @@ def kolibri_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, res: tor
         if res_out is not None:
             raise ValueError("res_out: needs res")
     elif res_out is None:
-        res_out = torch.empty_like(res)
+        res_out = _made(stream, torch.empty_like(res))
     if y is None and want_y:
-        y = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+        y = _made(stream, torch.empty((N, d), dtype=torch.bfloat16, device=dev))
     groups = (d + 127) // 128
     if y8 is None and want_fp8:
-        y8 = torch.empty((N, d), dtype=torch.float8_e4m3fn, device=dev)
+        y8 = _made(stream, torch.empty((N, d), dtype=torch.float8_e4m3fn, device=dev))
     if scales is None and y8 is not None:
-        scales = torch.empty((N, groups), dtype=torch.float32, device=dev)
+        scales = _made(stream, torch.empty((N, groups), dtype=torch.float32, device=dev))
     _need_all(index, (x, x.dtype, (N, d), "x"), (weight, weight.dtype, (d,), "weight"),
               (res, None if res is None else res.dtype, (N, d), "res"),
               (res_out, None if res is None else res.dtype, (N, d), "res_out"), (y, torch.bfloat16, (N, d), "y"),
@@ -766,9 +774,9 @@ def kolibri_rms_norm_grad(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     index = _on_current(h, "h")
     ht, gt, wt = _type_of(h, "h"), _type_of(gy, "gy"), _type_of(weight, "weight")
     if gx is None:
-        gx = torch.empty_like(h)
+        gx = _made(stream, torch.empty_like(h))
     if gweight is None and want_gweight:
-        gweight = torch.empty((d,), dtype=torch.float32, device=dev)
+        gweight = _made(stream, torch.empty((d,), dtype=torch.float32, device=dev))
     if ws is None and gweight is not None:
         n = int(load().kolibri_rms_norm_grad_workspace_size(N, d))
         ws = torch.empty((max(n, 1),), dtype=torch.uint8, device=dev)
@@ -798,13 +806,13 @@ def kolibri_balance_loss(z: torch.Tensor, ids: torch.Tensor, lam: float, seq_off
     if gz is None and want_gz:
         if accumulate:
             raise ValueError("gz: accumulate needs the gradient to add to")
-        gz = torch.empty((N, E), dtype=torch.float32, device=dev)
+        gz = _made(stream, torch.empty((N, E), dtype=torch.float32, device=dev))
     if loss is None:
-        loss = torch.empty((S,), dtype=torch.float32, device=dev)
+        loss = _made(stream, torch.empty((S,), dtype=torch.float32, device=dev))
     if counts is None:
-        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+        counts = _made(stream, torch.empty((S, E), dtype=torch.int32, device=dev))
     if prob is None:
-        prob = torch.empty((S, E), dtype=torch.float32, device=dev)
+        prob = _made(stream, torch.empty((S, E), dtype=torch.float32, device=dev))
     if ws is None:
         n = int(load().kolibri_balance_loss_workspace_size(N, E, S))
         ws = torch.empty((max(n, 1),), dtype=torch.uint8, device=dev)
@@ -832,7 +840,7 @@ def kolibri_balance_loss_grad(z: torch.Tensor, counts: torch.Tensor, K: int, lam
     if gz is None:
         if accumulate:
             raise ValueError("gz: accumulate needs the gradient to add to")
-        gz = torch.empty((N, E), dtype=torch.float32, device=dev)
+        gz = _made(stream, torch.empty((N, E), dtype=torch.float32, device=dev))
     _need_all(index, (z, torch.float32, (N, E), "z"), (counts, torch.int32, (S, E), "counts"),
               (seq_offsets, torch.int64, (S + 1,), "seq_offsets"), (grad_loss, torch.float32, (S,), "grad_loss"),
               (gz, torch.float32, (N, E), "gz"))
@@ -869,9 +877,9 @@ def kolibri_expert_ffn_fp8(x8: torch.Tensor, x_scale: torch.Tensor, perm: torch.
     if any((t is not None) != shared for t in (ss_gate_up, ws_down, ss_down)):
         raise ValueError("shared expert: ws_gate_up, ss_gate_up, ws_down and ss_down go together")
     if y is None:
-        y = torch.empty((N, d), dtype=torch.bfloat16, device=dev)
+        y = _made(stream, torch.empty((N, d), dtype=torch.bfloat16, device=dev))
     if ws is None:
-        ws = expert_ffn_fp8_workspace(N, d, F, K, shared, dev)
+        ws = _made(stream, expert_ffn_fp8_workspace(N, d, F, K, shared, dev))
     f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
     _need_all(index, (x8, f8, (N, d), "x8"), (x_scale, f32, (N, d // 128), "x_scale"), (perm, i32, (N * K,), "perm"),
               (offsets, torch.int64, (E + 1,), "offsets"), (inv, i32, (N * K,), "inv"), (gates, f32, (N, K), "gates"),

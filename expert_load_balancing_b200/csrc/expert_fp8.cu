@@ -6,7 +6,7 @@
 // bf16.  For slot p of expert e and token t:
 //   g, u  = sum over k blocks b of  xs[t,b] ws[e,.,b] (sum_{k in b} x8 w8)    fp32
 //   h     = SiLU(g) u, then per 128 units hs = max(amax|h|, 1e-30) / 448, h8 = e4m3(h / hs)
-//   o[p]  = sum over unit blocks b of  hs[p,b] wds[e,.,b] (sum h8 wd8)        fp32, rounded to bf16
+//   o[p]  = sum over unit blocks b of  hs[p,b] wds[e,.,b] (sum h8 wd8)        fp32, kept in fp16 (below)
 //   y[t]  = o_shared[t] + sum_k gates[t,k] o[inv[t K + k]]                    fp32, rounded to bf16
 //
 // The scales are arbitrary fp32 numbers per 128 values of k, so the tensor

@@ -556,9 +556,10 @@ KOLIBRI_API kolibri_status kolibri_expert_combine(const float *y_perm, const flo
  *   gz          [N, E] fp32, or NULL: no gradient
  *   ws          kolibri_balance_loss_workspace_size(N, E, S) bytes, 16-byte
  *               aligned; need not be initialised
- * K >= 1, K < E <= 512, E % 4 == 0, S E < 2^31.  Sums over tokens do not
+ * 1 <= K < E <= 512, K <= 16, E % 4 == 0, S E < 2^31.  Sums over tokens do not
  * depend on the order in which blocks run: the same inputs give the same bits
- * on the same GPU model.
+ * on the same GPU model, in the gradient too whether it is formed here or by
+ * kolibri_balance_loss_grad.
  */
 KOLIBRI_API size_t kolibri_balance_loss_workspace_size(int64_t N, int32_t E, int32_t S);
 KOLIBRI_API kolibri_status kolibri_balance_loss(const float *z, const int32_t *ids,
@@ -640,14 +641,18 @@ KOLIBRI_API kolibri_status kolibri_rms_norm_grad(const void *gy, int32_t gy_type
  * Arithmetic: products of e4m3 values accumulated on the tensor cores over 128
  * values of k, then scaled and summed in fp32.  h = SiLU(g) u in fp32 is held
  * in e4m3 with a scale max(amax |h|, 1e-30) / 448 per 128 units; an expert's
- * output is rounded once to bf16, multiplied by its gate and summed in fp32 in
- * the order shared, k = 0 .. K-1, and rounded to bf16.  Serving only: there is
- * no gradient.
+ * output is kept in fp32 or, above 64 rows, in fp16 with a power of two per 128
+ * columns (one rounding of 2^-12 of the 128 columns' largest), multiplied by its
+ * gate and summed in fp32 in the order shared, k = 0 .. K-1, and rounded to
+ * bf16.  Serving only: there is no gradient.
  * Shapes: d % 256 == 0, d <= 8192, F % 128 == 0, F <= 8192, E <= 512, K <= 16,
  * N (K + 1) < 2^31 - 512.  ws: kolibri_expert_ffn_fp8_workspace_size bytes
- * (about N (K + 1) (F + 2 d)), 16-byte aligned, need not be initialised.
- * Entries of perm or inv outside [0, N K) and offsets that do not run from 0
- * to N K without decreasing set KOLIBRI_ERR_DEVICE; y is then unspecified.
+ * (about N K d + N (K + 1) (F + 2 d)), 16-byte aligned, need not be
+ * initialised.  Calls of up to 64 rows (N (K + 1), N K without a shared expert)
+ * run in two launches that stream the weights row by row and do not read perm.
+ * Entries of perm or inv outside [0, N K) that are read, and offsets that do not
+ * run from 0 to N K without decreasing, set KOLIBRI_ERR_DEVICE; y is then
+ * unspecified (no access leaves the arrays).
  */
 KOLIBRI_API size_t kolibri_expert_ffn_fp8_workspace_size(int64_t N, int32_t d, int32_t F,
                                                          int32_t K, int32_t shared);
