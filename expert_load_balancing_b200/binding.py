@@ -691,7 +691,7 @@ def _need_all(index, *args):
     for t, dtype, shape, name in args:
         if t is None:
             continue
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
             raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{index}, got "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}"
                              f"{'' if t.is_contiguous() else ', not contiguous'}")

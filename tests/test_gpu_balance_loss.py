@@ -86,6 +86,8 @@ CASES = [
     (256, 384, 6, [0, 256]), (257, 260, 2, [0, 100, 100, 257]), (1000, 512, 16, [0, 1, 2, 3, 500, 1000]),
     (4096, 384, 6, [0, 4096]), (5003, 128, 8, [0, 17, 4000, 4000, 4001, 5003]), (700, 64, 1, list(range(0, 701))),
     (6000, 12, 5, [0, 2999, 6000]), (40001, 256, 4, [0, 12345, 40001]),
+    # more sequences than a block keeps boundaries of, most of them empty
+    (1500, 64, 2, [0] * 400 + sorted((7 * i) % 1501 for i in range(1501)) + [1500] * 9),
 ]
 
 
@@ -223,12 +225,13 @@ def test_refusals():
         B.kolibri_balance_loss_grad(z, ids, 4, 1e-3)
 
 
-def test_other_stream_and_graph():
-    N, E, K, cut = 3001, 384, 6, [0, 1000, 3001]
+@pytest.mark.parametrize("N,cut", [(3001, [0, 1000, 3001]), (500, [3, 500])])
+def test_other_stream_and_graph(N, cut):
+    E, K = 384, 6
     z, ids, seq, up = _inputs(N, E, K, cut, 9)
     want = B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq, grad_loss=up, want_gz=True)
     out = [torch.empty_like(t) for t in want]
-    ws = torch.empty(B.load().kolibri_balance_loss_workspace_size(N, E, 2), device="cuda", dtype=torch.uint8)
+    ws = torch.empty(B.load().kolibri_balance_loss_workspace_size(N, E, len(cut) - 1), device="cuda", dtype=torch.uint8)
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
 
@@ -248,4 +251,19 @@ def test_other_stream_and_graph():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want))
+    check_status()
+
+
+def test_rows_behind_32_bit_offsets():
+    """2.2e9 logits: the last rows come out as those rows do in a sequence of their own."""
+    N, E, K, tail = 4_300_000, 512, 2, 1000
+    z = torch.empty(N, E, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    ids = torch.randint(0, E, (N, K), device="cuda", dtype=torch.int32)
+    seq = torch.tensor([0, N - tail, N], device="cuda")
+    loss, counts, prob, gz = B.kolibri_balance_loss(z, ids, 1e-2, seq_offsets=seq, want_gz=True)
+    zt, it = z[-tail:].contiguous(), ids[-tail:].contiguous()
+    l2, c2, p2, g2 = B.kolibri_balance_loss(zt, it, 1e-2, want_gz=True)
+    assert torch.equal(counts[1], c2[0]) and torch.equal(gz[-tail:], g2)
+    assert ((prob[1] - p2[0]).abs() <= 2.0 ** -16 * p2[0]).all() and abs(float(loss[1] - l2[0])) <= 2.0 ** -15 * float(l2[0])
+    assert int(counts[0].sum()) == (N - tail) * K
     check_status()

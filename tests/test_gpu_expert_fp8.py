@@ -153,6 +153,7 @@ CASES = [
     # a few rows per expert, some of them with many
     (64, 2560, 512, 384, 6, True, False), (100, 512, 256, 128, 4, True, True), (65, 256, 128, 512, 1, True, False),
     (500, 768, 384, 64, 1, True, False), (12, 8192, 128, 64, 8, False, False), (12, 256, 8192, 64, 8, True, False),
+    (33, 256, 128, 1, 1, True, False), (300, 256, 128, 1, 1, False, False),
     # several tiles per block: every barrier goes round many times
     (20000, 256, 512, 6, 2, True, False), (4000, 2048, 256, 4, 2, False, False), (9000, 1024, 384, 3, 1, True, True),
 ]
@@ -295,4 +296,19 @@ def test_other_stream_and_graph():
             graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+    check_status()
+
+
+def test_rows_behind_32_bit_offsets():
+    """2.4e9 bytes of gathered rows, 4.8e9 of expert outputs: the last tokens come out as in a call of their own."""
+    N, d, F, E, K, tail = 155_000, 2560, 128, 16, 6, 40
+    c = _case(N, d, F, E, K, True, 9)
+    y = _call(c)
+    check_status()
+    t = dict(c)
+    for k in ("x8", "xs", "gates", "ids"):
+        t[k] = c[k].view(torch.uint8)[-tail:].view(F8).contiguous() if k == "x8" else c[k][-tail:].contiguous()
+    t["perm"], t["off"], t["inv"] = _group(t["ids"], E)
+    small = _call(t)
+    assert torch.equal(y[-tail:], small)
     check_status()

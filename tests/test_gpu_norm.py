@@ -202,6 +202,10 @@ def test_gradient(N, d, ht, gt, wt, gres):
     if gr is not None:
         B.kolibri_rms_norm_grad(gy, h, w, EPS, gres=gr, gx=gr)
         assert torch.equal(gr, gx)
+    if gt == ht:
+        y1 = gy.clone()
+        B.kolibri_rms_norm_grad(y1, h, w, EPS, gres=None, gx=y1)
+        assert torch.equal(y1, B.kolibri_rms_norm_grad(gy, h, w, EPS)[0])
     h1 = h.clone()
     B.kolibri_rms_norm_grad(gy, h1, w, EPS, gres=None, gx=h1)
     assert torch.equal(h1, B.kolibri_rms_norm_grad(gy, h, w, EPS)[0])
@@ -269,4 +273,21 @@ def test_other_stream_and_graph():
     for _ in range(2):
         graph.replay()
     same()
+    check_status()
+
+
+def test_rows_behind_32_bit_offsets():
+    """2.2e9 elements: the last rows come out as in a call of their own."""
+    N, d = 860_000, 2560
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.empty(N, d, device="cuda", dtype=BF).normal_(generator=g)
+    w = torch.ones(d, device="cuda", dtype=BF)
+    out = B.kolibri_rms_norm(x, w, EPS, res=x, want_fp8=True)
+    t = x[-5:].contiguous()
+    for a, b in zip(out, B.kolibri_rms_norm(t, w, EPS, res=t, want_fp8=True)):
+        assert torch.equal(a[-5:].view(torch.uint8), b.view(torch.uint8))
+    gx, _ = B.kolibri_rms_norm_grad(out[1], out[0], w, EPS, gres=x)
+    small, _ = B.kolibri_rms_norm_grad(out[1][-5:].contiguous(), out[0][-5:].contiguous(), w, EPS, gres=t)
+    # another block size sums a row in another order: fp32 sums of 2560 terms, then one bf16 rounding
+    assert ((gx[-5:].float() - small.float()).abs() <= 2.0 ** -7 * small.float().abs() + 1e-6).all()
     check_status()
