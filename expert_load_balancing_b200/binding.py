@@ -708,15 +708,20 @@ _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _raw_stream(stream, index):
     if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"stream: expected one of cuda:{index}, got one of {stream.device}")
         return stream.cuda_stream
     return _current_raw(index) if _current_raw else torch.cuda.current_stream(index).cuda_stream
 
 
-def _made(stream, t):
-    """A tensor allocated by the call itself (on the current stream): with a stream given, its memory is not handed out
-    again before that stream is through with it."""
-    if stream is not None:
-        t.record_stream(stream)
+def _made(stream, shape, dtype, dev):
+    """An array of the call's own.  With a stream given it is taken from that stream's memory (another stream's may still
+    be in use there) and not handed out again before the current stream, where the caller may read it, is through."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 
@@ -744,14 +749,14 @@ def kolibri_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, res: tor
         if res_out is not None:
             raise ValueError("res_out: needs res")
     elif res_out is None:
-        res_out = _made(stream, torch.empty_like(res))
+        res_out = _made(stream, res.shape, res.dtype, dev)
     if y is None and want_y:
-        y = _made(stream, torch.empty((N, d), dtype=torch.bfloat16, device=dev))
+        y = _made(stream, (N, d), torch.bfloat16, dev)
     groups = (d + 127) // 128
     if y8 is None and want_fp8:
-        y8 = _made(stream, torch.empty((N, d), dtype=torch.float8_e4m3fn, device=dev))
+        y8 = _made(stream, (N, d), torch.float8_e4m3fn, dev)
     if scales is None and y8 is not None:
-        scales = _made(stream, torch.empty((N, groups), dtype=torch.float32, device=dev))
+        scales = _made(stream, (N, groups), torch.float32, dev)
     _need_all(index, (x, x.dtype, (N, d), "x"), (weight, weight.dtype, (d,), "weight"),
               (res, None if res is None else res.dtype, (N, d), "res"),
               (res_out, None if res is None else res.dtype, (N, d), "res_out"), (y, torch.bfloat16, (N, d), "y"),
@@ -774,12 +779,12 @@ def kolibri_rms_norm_grad(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     index = _on_current(h, "h")
     ht, gt, wt = _type_of(h, "h"), _type_of(gy, "gy"), _type_of(weight, "weight")
     if gx is None:
-        gx = _made(stream, torch.empty_like(h))
+        gx = _made(stream, h.shape, h.dtype, dev)
     if gweight is None and want_gweight:
-        gweight = _made(stream, torch.empty((d,), dtype=torch.float32, device=dev))
+        gweight = _made(stream, (d,), torch.float32, dev)
     if ws is None and gweight is not None:
         n = int(load().kolibri_rms_norm_grad_workspace_size(N, d))
-        ws = torch.empty((max(n, 1),), dtype=torch.uint8, device=dev)
+        ws = _made(stream, (max(n, 1),), torch.uint8, dev)
     _need_all(index, (h, h.dtype, (N, d), "h"), (gy, gy.dtype, (N, d), "gy"), (weight, weight.dtype, (d,), "weight"),
               (gres, h.dtype, (N, d), "gres"), (gx, h.dtype, (N, d), "gx"), (gweight, torch.float32, (d,), "gweight"),
               (ws, torch.uint8, (0 if ws is None else ws.numel(),), "ws"))
@@ -787,6 +792,13 @@ def kolibri_rms_norm_grad(gy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
            load().kolibri_rms_norm_grad(_addr(gy), gt, _addr(h), ht, _addr(weight), wt, eps, _addr(gres), N, d, _addr(gx),
                                         _addr(gweight), _addr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, index)))
     return gx, gweight
+
+
+def _sequences(seq_offsets):
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    if S < 1:
+        raise ValueError("seq_offsets: expected the boundaries of at least one sequence")
+    return S
 
 
 def kolibri_balance_loss(z: torch.Tensor, ids: torch.Tensor, lam: float, seq_offsets: torch.Tensor | None = None,
@@ -800,22 +812,22 @@ def kolibri_balance_loss(z: torch.Tensor, ids: torch.Tensor, lam: float, seq_off
     same pass writes the gradient of sum_s grad_loss[s] loss[s], or adds it to gz with accumulate."""
     N, E = z.shape
     K = ids.shape[1]
-    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    S = _sequences(seq_offsets)
     dev = z.device
     index = _on_current(z, "z")
     if gz is None and want_gz:
         if accumulate:
             raise ValueError("gz: accumulate needs the gradient to add to")
-        gz = _made(stream, torch.empty((N, E), dtype=torch.float32, device=dev))
+        gz = _made(stream, (N, E), torch.float32, dev)
     if loss is None:
-        loss = _made(stream, torch.empty((S,), dtype=torch.float32, device=dev))
+        loss = _made(stream, (S,), torch.float32, dev)
     if counts is None:
-        counts = _made(stream, torch.empty((S, E), dtype=torch.int32, device=dev))
+        counts = _made(stream, (S, E), torch.int32, dev)
     if prob is None:
-        prob = _made(stream, torch.empty((S, E), dtype=torch.float32, device=dev))
+        prob = _made(stream, (S, E), torch.float32, dev)
     if ws is None:
         n = int(load().kolibri_balance_loss_workspace_size(N, E, S))
-        ws = torch.empty((max(n, 1),), dtype=torch.uint8, device=dev)
+        ws = _made(stream, (max(n, 1),), torch.uint8, dev)
     _need_all(index, (z, torch.float32, (N, E), "z"), (ids, torch.int32, (N, K), "ids"),
               (seq_offsets, torch.int64, (S + 1,), "seq_offsets"), (grad_loss, torch.float32, (S,), "grad_loss"),
               (gz, torch.float32, (N, E), "gz"), (loss, torch.float32, (S,), "loss"),
@@ -834,13 +846,13 @@ def kolibri_balance_loss_grad(z: torch.Tensor, counts: torch.Tensor, K: int, lam
                               accumulate: bool = False, stream=None) -> torch.Tensor:
     """The gradient of kolibri_balance_loss from the counts [S, E] it wrote: gz [N, E] fp32, added to with accumulate."""
     N, E = z.shape
-    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    S = _sequences(seq_offsets)
     dev = z.device
     index = _on_current(z, "z")
     if gz is None:
         if accumulate:
             raise ValueError("gz: accumulate needs the gradient to add to")
-        gz = _made(stream, torch.empty((N, E), dtype=torch.float32, device=dev))
+        gz = _made(stream, (N, E), torch.float32, dev)
     _need_all(index, (z, torch.float32, (N, E), "z"), (counts, torch.int32, (S, E), "counts"),
               (seq_offsets, torch.int64, (S + 1,), "seq_offsets"), (grad_loss, torch.float32, (S,), "grad_loss"),
               (gz, torch.float32, (N, E), "gz"))
@@ -877,9 +889,10 @@ def kolibri_expert_ffn_fp8(x8: torch.Tensor, x_scale: torch.Tensor, perm: torch.
     if any((t is not None) != shared for t in (ss_gate_up, ws_down, ss_down)):
         raise ValueError("shared expert: ws_gate_up, ss_gate_up, ws_down and ss_down go together")
     if y is None:
-        y = _made(stream, torch.empty((N, d), dtype=torch.bfloat16, device=dev))
+        y = _made(stream, (N, d), torch.bfloat16, dev)
     if ws is None:
-        ws = _made(stream, expert_ffn_fp8_workspace(N, d, F, K, shared, dev))
+        n = int(load().kolibri_expert_ffn_fp8_workspace_size(N, d, F, K, 1 if shared else 0))
+        ws = _made(stream, (max(n, 1),), torch.uint8, dev)
     f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
     _need_all(index, (x8, f8, (N, d), "x8"), (x_scale, f32, (N, d // 128), "x_scale"), (perm, i32, (N * K,), "perm"),
               (offsets, torch.int64, (E + 1,), "offsets"), (inv, i32, (N * K,), "inv"), (gates, f32, (N, K), "gates"),

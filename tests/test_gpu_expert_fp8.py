@@ -9,8 +9,10 @@ magnitudes A, so g and u carry d 2^-24 (Ag, Au), and with |SiLU'| < 1.1
   |dh| <= d 2^-24 (1.1 |u| Ag + |SiLU(g)| Au) + 2^-19 |h|
 (the fast exponential and division: under 32 units of 2^-24).  The scale of a
 group moves with its largest |h|: by max |dh| / 448 and two roundings.  Then y:
-an expert's o carries F 2^-24 of the magnitudes and 2^-8 |o|, the sum over K + 1
-of them (K + 1) 2^-24 and y itself 2^-8 |y|."""
+an expert's o carries F 2^-24 of the magnitudes and, kept in fp16 with its
+group's largest in [2^14, 2^15), 2^-11 |o| or, where that is below the normal
+numbers, 2^-25 of 2^-14 of the group's largest; the sum over K + 1 of them (K + 1)
+2^-24 and y itself 2^-8 |y|."""
 import math
 
 import pytest
@@ -128,7 +130,9 @@ def _check(c, y, ws):
         assert float(err) <= 1.0, ("h", e, float(err))
         o[a:b] = hq @ wd.T
         mag[a:b] = hq.abs() @ wd.abs().T
-    do = F * 2.0 ** -24 * mag + 2.0 ** -8 * o.abs()
+    top = o.abs().view(rows, d // 128, 128).amax(2).repeat_interleave(128, 1)
+    do = F * 2.0 ** -24 * mag
+    do = do + 2.0 ** -11 * (o.abs() + do) + 2.0 ** -39 * (top + do)
     gates = c["gates"].double()
     at = c["inv"].long().view(N, K)
     want = (o[at] * gates[..., None]).sum(1)

@@ -185,3 +185,47 @@ def test_calls_on_a_stream_of_their_own_with_buffers_of_theirs():
             assert torch.equal(row[0], bufs[i]["ffn"])
             assert all(torch.equal(a, b) for a, b in zip(row, got[i][0]))
     check_status()
+
+
+@pytest.mark.parametrize("which", ["norm", "norm_grad", "balance", "balance_grad", "experts"])
+def test_memory_of_a_call_on_another_stream(which):
+    """A call on a busy stream that allocates what it needs.  What the current stream allocates meanwhile is not the
+    call's workspace, and memory that the current stream has still to read is not given to the call."""
+    L = Layer(512, 256, 64, 2, 6)
+    N = 900
+    x = L.rnd(N, 512).to(BF)
+    b = L.buffers(N)
+    L.forward(x, x, B.workspace(B.KOLIBRI_OP_PERMUTE, N, L.E, L.K), B.expert_ffn_fp8_workspace(N, 512, 256, 2, True), b)
+    counts = torch.bincount(b["ids"].reshape(-1).long(), minlength=L.E).to(torch.int32).view(1, L.E)
+    lib = B.load()
+    call, ws_bytes = {
+        "norm": (lambda st: B.kolibri_rms_norm(x, L.norm, EPS, res=x, want_fp8=True, stream=st), 4),
+        "norm_grad": (lambda st: B.kolibri_rms_norm_grad(b["y"], b["res"], L.norm, EPS, stream=st),
+                      lib.kolibri_rms_norm_grad_workspace_size(N, 512)),
+        "balance": (lambda st: B.kolibri_balance_loss(b["z"], b["ids"], 0.1, want_gz=True, stream=st),
+                    lib.kolibri_balance_loss_workspace_size(N, L.E, 1)),
+        "balance_grad": (lambda st: (B.kolibri_balance_loss_grad(b["z"], counts, 2, 0.1, stream=st),), 4),
+        "experts": (lambda st: (B.kolibri_expert_ffn_fp8(b["y8"], b["s"], b["perm"], b["offsets"], b["inv"], b["gates"],
+                                                         L.gu, L.sgu, L.dn, L.sdn, L.gus, L.sgus, L.dns, L.sdns, stream=st),),
+                    lib.kolibri_expert_ffn_fp8_workspace_size(N, 512, 256, 2, 1)),
+    }[which]
+    want = call(None)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(40_000_000)
+    got = call(st)
+    mine = [torch.full((ws_bytes,), 3, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all((m == 3).all() for m in mine)
+    assert all(torch.equal(a.view(torch.uint8), w.view(torch.uint8)) for a, w in zip(got, want))
+    held = [torch.full((w.numel() * w.element_size(),), 5, dtype=torch.uint8, device="cuda") for w in want for _ in range(2)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(40_000_000)
+    copies = [h.clone() for h in held]
+    del held
+    got = call(st)
+    torch.cuda.synchronize()
+    assert all((c == 5).all() for c in copies)
+    assert all(torch.equal(a.view(torch.uint8), w.view(torch.uint8)) for a, w in zip(got, want))
+    check_status()

@@ -6,6 +6,8 @@ import math
 import pytest
 import torch
 
+from expert_load_balancing_b200 import binding as B
+
 INVALID, SHAPE, SMALL = 1, 2, 3
 F = 0x10000        # a 16-byte aligned address that is never dereferenced
 ODD = 0x10004      # a misaligned one
@@ -95,6 +97,16 @@ def test_python_calls_refuse_cpu_tensors_and_wrong_types():
         B.kolibri_balance_loss(x, torch.zeros(4, 2, dtype=torch.int32), 1e-3)
     with pytest.raises((ValueError, RuntimeError)):
         B.kolibri_balance_loss_grad(x, torch.zeros(1, 64, dtype=torch.int32), 2, 1e-3)
+
+
+@pytest.mark.parametrize("bounds", [[], [0]])
+def test_python_calls_refuse_boundaries_of_no_sequence(bounds):
+    seq = torch.tensor(bounds, dtype=torch.int64)
+    z, ids, counts = torch.zeros(8, 16), torch.zeros(8, 2, dtype=torch.int32), torch.zeros(1, 16, dtype=torch.int32)
+    with pytest.raises(ValueError, match="seq_offsets"):
+        B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq)
+    with pytest.raises(ValueError, match="seq_offsets"):
+        B.kolibri_balance_loss_grad(z, counts, 2, 1e-3, seq_offsets=seq)
 
 
 def test_expert_fp8_checks(lib):
