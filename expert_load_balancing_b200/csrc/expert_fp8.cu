@@ -25,9 +25,17 @@
 // requests queue behind the bulk loads, the projection took 1615 us instead of
 // 514 (16384 tokens, 384 experts).  The shared expert is one more group of the
 // same launch.  o is kept in fp16 with a power of two per 1 x 128 group, which
-// costs one rounding of 2^-12 relative to the group's largest value: it is
-// written and read once, N K d values, and in fp32 would be the largest traffic
-// of the layer.
+// costs each value one rounding of at most 2^-11 of itself (an eighth of y's own
+// to bf16; values below 2^-28 of the group's largest lose more): it is written
+// and read once, N K d values, and in fp32 would be the largest traffic of the
+// layer.
+//
+// Measured (d = 2560, F = 512, 6 of 384 experts and the shared one): 16384 tokens
+// 873-890 us in a burst (gather 65, gate/up 412, down 282, combine 113), 1040 in
+// a loop of seconds, where the power limit takes the clock to 1.53 GHz.  What
+// bounds the two products is the SM's shared memory and tensor pipe in turn: loads
+// alone take 266 and 208 us, loads and MMAs 340 and 258, MMAs alone 205 and 161,
+// the sums alone 289 and 204.  64 tokens 172 us, bound by the weights' 0.95 GB.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -556,6 +556,7 @@ KOLIBRI_API kolibri_status kolibri_expert_combine(const float *y_perm, const flo
  *   gz          [N, E] fp32, or NULL: no gradient
  *   ws          kolibri_balance_loss_workspace_size(N, E, S) bytes, 16-byte
  *               aligned; need not be initialised
+ * Outputs must not overlap one another, the inputs or ws.
  * 1 <= K < E <= 512, K <= 16, E % 4 == 0, S E < 2^31.  Sums over tokens do not
  * depend on the order in which blocks run: the same inputs give the same bits
  * on the same GPU model, in the gradient too whether it is formed here or by
@@ -597,7 +598,8 @@ KOLIBRI_API kolibri_status kolibri_balance_loss_grad(const float *z, const int32
  * At least one of y and y8.  res_out may be res or x, and y may be x, where the
  * types agree (in place); outputs must not overlap otherwise.
  * d % 8 == 0, 8 <= d <= 16384, eps >= 0 (a row of zeros with eps = 0 is not a
- * number).
+ * number).  The squares are summed in fp32: a row whose sum of h^2 leaves fp32's
+ * range (|h| about 1e19) has y = 0.
  */
 KOLIBRI_API kolibri_status kolibri_rms_norm(const void *x, int32_t x_type, const void *res,
                                             int32_t res_type, const void *weight,
@@ -642,9 +644,10 @@ KOLIBRI_API kolibri_status kolibri_rms_norm_grad(const void *gy, int32_t gy_type
  * values of k, then scaled and summed in fp32.  h = SiLU(g) u in fp32 is held
  * in e4m3 with a scale max(amax |h|, 1e-30) / 448 per 128 units; an expert's
  * output is kept in fp32 or, above 64 rows, in fp16 with a power of two per 128
- * columns (one rounding of 2^-12 of the 128 columns' largest), multiplied by its
- * gate and summed in fp32 in the order shared, k = 0 .. K-1, and rounded to
- * bf16.  Serving only: there is no gradient.
+ * columns (one rounding of at most 2^-11 of each value, or of 2^-39 of the 128
+ * columns' largest where that is more), multiplied by its gate and summed in
+ * fp32 in the order shared, k = 0 .. K-1, and rounded to bf16.  Serving only:
+ * there is no gradient.
  * Shapes: d % 256 == 0, d <= 8192, F % 128 == 0, F <= 8192, E <= 512, K <= 16,
  * N (K + 1) < 2^31 - 512.  ws: kolibri_expert_ffn_fp8_workspace_size bytes
  * (about N K d + N (K + 1) (F + 2 d)), 16-byte aligned, need not be
