@@ -158,7 +158,7 @@ struct LossParams {
 // and gradient: 575 us at four blocks, 640 at two, 765 at the three of an
 // unbounded register count).  With four float4s a lane the sums and logits need
 // more than the 64 registers of four blocks, and two without spills beat three
-// with (E = 128, 65,536 rows in 37 sequences, loss and then gradient, in a graph:
+// with (E = 128, 65,536 rows in 61 sequences, loss and then gradient, in a graph:
 // 32.8 us, 36.9).
 template <int V>
 struct LossBlocks {
