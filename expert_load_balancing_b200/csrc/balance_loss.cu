@@ -11,18 +11,19 @@
 //
 // The counts carry no gradient (they come from the selection).  As sum_j p_tj
 // = 1, f enters as f - 1 throughout, which keeps the difference in the bracket
-// exact to fp32 when the loads are nearly even, and L = lambda (1 + mean_t
-// dot_t) with dot_t = sum_j (f_j - 1) p_tj, the sum that the gradient needs
-// anyway.
+// exact to fp32 when the loads are nearly even: dot_t = sum_j (f_j - 1) p_tj,
+// and at even loads L is lambda and the gradient 0 to the last bit.
 //
 // Measured (E = 384, 6 of them chosen, loss and gradient): 1,048,576 rows 576 us,
 // 0.86 of a copy's bandwidth for the 3.25 GB: counts 13, the pass 550, the finish
 // 7, and the gaps.
 //
-// The gradient needs f, which comes from the ids alone, and not P: so the
-// counts are formed first (a read of the ids) and ONE pass over Z then forms
-// P, L and dL/dZ.  Bound by HBM: 4 E bytes of Z read and, with the gradient,
-// 4 E bytes written per token.
+// The gradient needs f, which comes from the ids alone, and not P: so with the
+// gradient the counts are formed first (a read of the ids) and ONE pass over Z
+// then forms P and dL/dZ.  Without it nothing in the pass needs f, and the pass
+// counts too.  L = lambda (1 - r + sum_e (f_e - 1) P_e) comes from the sums of
+// both, where r is the share of rows without p.  Bound by HBM: 4 E bytes of Z
+// read and, with the gradient, 4 E bytes written per token.
 //
 // Sums over tokens: fp32 per warp over the rows of one block, then the blocks'
 // shares in fp64 in a fixed order; counts are integers.  Nothing depends on
@@ -78,6 +79,43 @@ struct Seqs {
   }
 };
 
+// Offsets that decrease or leave [0, N] are reported (block 0).
+__device__ __forceinline__ void check_seqs(const Seqs& q) {
+  if (blockIdx.x == 0 && q.seq)
+    for (int s = threadIdx.x; s <= q.S; s += kLossThreads) {
+      const int64_t v = q.seq[s];
+      if (v < 0 || v > q.N || (s > 0 && q.seq[s - 1] > v)) raise_status(kStatusBadInput);
+    }
+}
+
+// hist[e] += the slots of the rows [lo, hi) that are routed to e.
+__device__ __forceinline__ void count_rows(const int32_t* ids, int64_t lo, int64_t hi, int E, int K, int32_t* hist) {
+  const int64_t j1 = hi * K;
+  for (int64_t j = lo * K + threadIdx.x; j < j1; j += kCountAhead * kLossThreads) {
+    int32_t e[kCountAhead];
+#pragma unroll
+    for (int i = 0; i < kCountAhead; ++i)
+      if (j + i * kLossThreads < j1) e[i] = __ldcs(ids + j + i * kLossThreads);
+#pragma unroll
+    for (int i = 0; i < kCountAhead; ++i)
+      if (j + i * kLossThreads < j1) {
+        if (e[i] >= 0 && e[i] < E) atomicAdd(&hist[e[i]], 1);
+        else raise_status(kStatusBadInput);
+      }
+  }
+}
+
+// counts += hist, hist = 0.
+__device__ __forceinline__ void flush_counts(int32_t* hist, int E, int32_t* counts) {
+  for (int e = threadIdx.x; e < E; e += kLossThreads) {
+    const int32_t c = hist[e];
+    if (c) {
+      atomicAdd(&counts[e], c);
+      hist[e] = 0;
+    }
+  }
+}
+
 // counts [S][E] += the slots of this block's rows.  counts is zero on entry.
 __global__ void __launch_bounds__(kLossThreads) seq_count_kernel(const int32_t* ids, Seqs given, int E, int K,
                                                                  int64_t chunk, int32_t* counts) {
@@ -87,49 +125,28 @@ __global__ void __launch_bounds__(kLossThreads) seq_count_kernel(const int32_t* 
   const int64_t r0 = blockIdx.x * chunk;
   const int64_t r1 = r0 + chunk < q.N ? r0 + chunk : q.N;
   for (int e = threadIdx.x; e < E; e += kLossThreads) hist[e] = 0;
-  if (blockIdx.x == 0 && q.seq)
-    for (int s = threadIdx.x; s <= q.S; s += kLossThreads) {
-      const int64_t v = q.seq[s];
-      if (v < 0 || v > q.N || (s > 0 && q.seq[s - 1] > v)) raise_status(kStatusBadInput);
-    }
+  check_seqs(q);
   __syncthreads();
   for (int s = q.find(r0); s < q.S; ++s) {
     const int64_t b = q.at(s), e_ = q.at(s + 1);
     if (b >= r1) break;
     const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
     if (lo >= hi) continue;
-    const int64_t j1 = hi * K;
-    for (int64_t j = lo * K + threadIdx.x; j < j1; j += kCountAhead * kLossThreads) {
-      int32_t e[kCountAhead];
-#pragma unroll
-      for (int i = 0; i < kCountAhead; ++i)
-        if (j + i * kLossThreads < j1) e[i] = __ldcs(ids + j + i * kLossThreads);
-#pragma unroll
-      for (int i = 0; i < kCountAhead; ++i)
-        if (j + i * kLossThreads < j1) {
-          if (e[i] >= 0 && e[i] < E) atomicAdd(&hist[e[i]], 1);
-          else raise_status(kStatusBadInput);
-        }
-    }
+    count_rows(ids, lo, hi, E, K, hist);
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kLossThreads) {
-      const int32_t c = hist[e];
-      if (c) {
-        atomicAdd(&counts[static_cast<int64_t>(s) * E + e], c);
-        hist[e] = 0;
-      }
-    }
+    flush_counts(hist, E, counts + static_cast<int64_t>(s) * E);
     __syncthreads();
   }
 }
 
 struct LossParams {
   const float* z;
-  const int32_t* counts;    // [S, E]
+  const int32_t* ids;       // [N, K]: counted in the pass without the gradient
+  int32_t* counts;          // [S, E]
   const float* grad_loss;   // [S] or null (ones)
   float* gz;                // [N, E]
   float* part;              // [chunks + S][E]: sums of p
-  double* dots;             // [chunks + S]: sums of dot_t
+  double* none;             // [chunks + S]: rows without p
   Seqs q;
   int64_t chunk;
   int E, K;
@@ -166,9 +183,10 @@ struct LossBlocks {
 };
 
 // Rows [lo, hi) of sequence s, which is rows [b, e_), with its counts: writes
-// their gradient, and leaves the warps' shares of P and of sum dot in psum and
-// dsum (all threads of the block; ends with a barrier if kProb).
-template <int L, int V, bool kSoftmax, bool kProb, bool kGrad>
+// their gradient, and leaves the warps' shares of P in psum and of sum dot (kDots)
+// or of the number of rows without p in dsum (all threads of the block; ends with
+// a barrier if kProb).
+template <int L, int V, bool kSoftmax, bool kProb, bool kGrad, bool kDots>
 __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* counts, int s, int64_t b, int64_t e_,
                                           int64_t lo, int64_t hi, float* psum, double* dsum) {
   constexpr int kRows = 32 / L;          // rows of a warp at once
@@ -182,7 +200,7 @@ __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* co
   for (int j = 0; j < V; ++j) {
     const int c4 = lane + L * j;
     int4 c = make_int4(0, 0, 0, 0);
-    if (c4 < E4) c = reinterpret_cast<const int4*>(counts)[c4];
+    if ((kGrad || kDots) && c4 < E4) c = reinterpret_cast<const int4*>(counts)[c4];
     fr[4 * j + 0] = static_cast<float>(static_cast<int64_t>(c.x) * p.E - slots) * per_slot;
     fr[4 * j + 1] = static_cast<float>(static_cast<int64_t>(c.y) * p.E - slots) * per_slot;
     fr[4 * j + 2] = static_cast<float>(static_cast<int64_t>(c.z) * p.E - slots) * per_slot;
@@ -239,7 +257,8 @@ __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* co
     const float inv = none ? 0.0f : rcp_fast(sum);
     dot = __fmul_rn(dot, inv);          // uncontracted: the same bits in every form of the pass
     if constexpr (kProb) {
-      dot_sum += !there ? 0.0f : none ? -1.0f : dot;         // a row without p adds nothing to L
+      if constexpr (kDots) dot_sum += !there ? 0.0f : none ? -1.0f : dot;       // a row without p adds nothing to L
+      else dot_sum += there && none ? 1.0f : 0.0f;
 #pragma unroll
       for (int i = 0; i < 4 * V; ++i) acc[i] = fmaf(z[i], inv, acc[i]);
     }
@@ -286,9 +305,12 @@ __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* co
   }
 }
 
+// kProb && !kGrad: the pass counts too; counts is zero on entry.
 template <int L, int V, bool kSoftmax, bool kProb, bool kGrad>
 __global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_loss_kernel(const LossParams p) {
+  constexpr bool kCount = kProb && !kGrad;
   __shared__ float psum[kProb ? kLossWarps * kMaxE : 1];
+  __shared__ int32_t hist[kCount ? kMaxE : 1];
   __shared__ double dsum[kLossWarps];
   const int E4 = p.E >> 2;
   __shared__ int64_t seq_s[kSeqCache];
@@ -296,6 +318,11 @@ __global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_l
   const int64_t r1 = r0 + p.chunk < p.q.N ? r0 + p.chunk : p.q.N;
   pdl_wait();          // the counts
   const Seqs q = p.q.cached(seq_s);
+  if constexpr (kCount) {
+    check_seqs(q);
+    for (int e = threadIdx.x; e < p.E; e += kLossThreads) hist[e] = 0;
+    __syncthreads();
+  }
   if constexpr (kGrad) {
     // rows of the chunk before the first and behind the last sequence have no gradient
     if (!p.accumulate) {
@@ -312,7 +339,10 @@ __global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_l
     if (b >= r1) break;
     const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
     if (lo >= hi) continue;
-    loss_rows<L, V, kSoftmax, kProb, kGrad>(p, p.counts + static_cast<int64_t>(s) * p.E, s, b, e_, lo, hi, psum, dsum);
+    int32_t* const counts = p.counts + static_cast<int64_t>(s) * p.E;
+    if constexpr (kCount) count_rows(p.ids, lo, hi, p.E, p.K, hist);
+    loss_rows<L, V, kSoftmax, kProb, kGrad, false>(p, counts, s, b, e_, lo, hi, psum, dsum);
+    if constexpr (kCount) flush_counts(hist, p.E, counts);
     if constexpr (kProb) {
       const int64_t slot = blockIdx.x + s;
       for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
@@ -325,62 +355,12 @@ __global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_l
         double t = 0.0;
 #pragma unroll
         for (int w = 0; w < kLossWarps; ++w) t += dsum[w];
-        p.dots[slot] = t;
+        p.none[slot] = t;
       }
       __syncthreads();
     }
   }
 }
-
-// prob[s][e] and loss[s] from the blocks' shares: a block per sequence and 32
-// experts, 16 shares at a time, fp64, fixed order.
-constexpr int kFinishRows = 16;
-__global__ void __launch_bounds__(32 * kFinishRows) balance_finish_kernel(const LossParams p, float* prob, float* loss) {
-  __shared__ double buf[kFinishRows][32];
-  pdl_wait();
-  const int tiles = (p.E + 31) / 32;
-  const int s = blockIdx.x / tiles, tile = blockIdx.x - s * tiles;
-  const int e = tile * 32 + threadIdx.x;
-  const int64_t b = p.q.at(s), en = p.q.at(s + 1);
-  const int64_t n = en > b ? en - b : 0;
-  const int64_t c0 = n ? b / p.chunk : 0, c1 = n ? (en - 1) / p.chunk + 1 : 0;   // chunks that hold rows of s
-  double t = 0.0;
-  if (e < p.E)
-#pragma unroll 4
-    for (int64_t c = c0 + threadIdx.y; c < c1; c += kFinishRows) t += p.part[(c + s) * p.E + e];
-  buf[threadIdx.y][threadIdx.x] = t;
-  __syncthreads();
-  if (threadIdx.y == 0 && e < p.E) {
-    t = 0.0;
-#pragma unroll
-    for (int r = 0; r < kFinishRows; ++r) t += buf[r][threadIdx.x];
-    prob[static_cast<int64_t>(s) * p.E + e] = n ? static_cast<float>(t / static_cast<double>(n)) : 0.0f;
-  }
-  if (tile == 0) {
-    __syncthreads();
-    t = 0.0;
-    for (int64_t c = c0 + threadIdx.y * 32 + threadIdx.x; c < c1; c += 32 * kFinishRows) t += p.dots[c + s];
-    buf[threadIdx.y][threadIdx.x] = t;
-    __syncthreads();
-    if (threadIdx.y == 0) {
-      t = 0.0;
-#pragma unroll
-      for (int r = 0; r < kFinishRows; ++r) t += buf[r][threadIdx.x];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      if (threadIdx.x == 0) loss[s] = n ? static_cast<float>(p.lambda * (1.0 + t / static_cast<double>(n))) : 0.0f;
-    }
-  }
-}
-
-// A small batch of one sequence: one launch, a cluster of eight blocks that
-// hold the counts and the shares of P in shared memory and read one another's.
-// The four launches of the other form cost 12 us whatever the size; 256 rows of
-// 384 take 10.3 (in a graph), most of it the three cluster barriers and the
-// chains from ids to counts to loss.  Up to 1024 rows: each of the eight SMs then
-// reads at most 128 rows (E = 384: 197 KB, about 2 us).
-constexpr int kClusterBlocks = 8;
-constexpr int64_t kSmallRows = 1024;
 
 __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
   uint32_t r;
@@ -400,6 +380,80 @@ __device__ __forceinline__ double remote_f64(const void* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
+// prob[s][e] and loss[s] from the blocks' shares and the counts: a cluster per
+// sequence, a block of it per 64 experts, 16 shares at a time, fp64, fixed order.
+constexpr int kFinishRows = 16;
+constexpr int kFinishCols = 64;
+static_assert(kMaxE / kFinishCols <= 8, "a cluster of at most eight blocks");
+__global__ void __launch_bounds__(32 * kFinishRows) balance_finish_kernel(const LossParams p, float* prob, float* loss) {
+  __shared__ double buf[kFinishRows][kFinishCols];
+  __shared__ double dot_s;
+  pdl_wait();
+  const int tiles = (p.E + kFinishCols - 1) / kFinishCols;
+  const int s = blockIdx.x / tiles, tile = blockIdx.x - s * tiles;       // tile: the rank in the cluster
+  const int e = tile * kFinishCols + 2 * threadIdx.x;                    // and e + 1: E is a multiple of 4
+  const int64_t b = p.q.at(s), en = p.q.at(s + 1);
+  const int64_t n = en > b ? en - b : 0;
+  const int64_t c0 = n ? b / p.chunk : 0, c1 = n ? (en - 1) / p.chunk + 1 : 0;   // chunks that hold rows of s
+  double t0 = 0.0, t1 = 0.0;
+  if (e < p.E)
+#pragma unroll 4
+    for (int64_t c = c0 + threadIdx.y; c < c1; c += kFinishRows) {
+      const float2 v = *reinterpret_cast<const float2*>(p.part + (c + s) * p.E + e);
+      t0 += v.x;
+      t1 += v.y;
+    }
+  buf[threadIdx.y][2 * threadIdx.x] = t0;
+  buf[threadIdx.y][2 * threadIdx.x + 1] = t1;
+  double none = 0.0;                     // of the last warp: its chain runs beside the first one's
+  if (threadIdx.y == kFinishRows - 1 && tile == 0) {
+    for (int64_t c = c0 + threadIdx.x; c < c1; c += 32) none += p.none[c + s];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) none += __shfl_xor_sync(0xffffffffu, none, o);
+  }
+  __syncthreads();
+  if (threadIdx.y == 0) {
+    double dot = 0.0;
+    if (e < p.E) {
+      t0 = t1 = 0.0;
+#pragma unroll
+      for (int r = 0; r < kFinishRows; ++r) {
+        t0 += buf[r][2 * threadIdx.x];
+        t1 += buf[r][2 * threadIdx.x + 1];
+      }
+      const double mean = n ? 1.0 / static_cast<double>(n) : 0.0;
+      t0 *= mean;
+      t1 *= mean;
+      *reinterpret_cast<float2*>(prob + static_cast<int64_t>(s) * p.E + e) =
+          make_float2(static_cast<float>(t0), static_cast<float>(t1));
+      const int2 c = *reinterpret_cast<const int2*>(p.counts + static_cast<int64_t>(s) * p.E + e);
+      const int64_t slots = n * p.K;
+      dot = static_cast<double>(static_cast<int64_t>(c.x) * p.E - slots) * t0 +
+            static_cast<double>(static_cast<int64_t>(c.y) * p.E - slots) * t1;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (threadIdx.x == 0) dot_s = dot;
+  }
+  cluster_barrier();
+  if (tile == 0 && threadIdx.y == kFinishRows - 1 && threadIdx.x == 0) {
+    double dot = 0.0;
+    for (int r = 0; r < tiles; ++r) dot += remote_f64(&dot_s, r);
+    const double rows = static_cast<double>(n);
+    loss[s] = n ? static_cast<float>(p.lambda * (1.0 - none / rows + dot / (rows * p.K))) : 0.0f;
+  }
+  cluster_barrier();                     // no block leaves while another reads its shared memory
+}
+
+// A small batch of one sequence: one launch, a cluster of eight blocks that
+// hold the counts and the shares of P in shared memory and read one another's.
+// The four launches of the other form cost 12 us whatever the size; 256 rows of
+// 384 take 10.3 (in a graph), most of it the three cluster barriers and the
+// chains from ids to counts to loss.  Up to 1024 rows: each of the eight SMs then
+// reads at most 128 rows (E = 384: 197 KB, about 2 us).
+constexpr int kClusterBlocks = 8;
+constexpr int64_t kSmallRows = 1024;
 
 template <int L, int V, bool kSoftmax, bool kGrad>
 __global__ void __launch_bounds__(kLossThreads) balance_small_kernel(const LossParams p, const int32_t* ids,
@@ -443,7 +497,7 @@ __global__ void __launch_bounds__(kLossThreads) balance_small_kernel(const LossP
   if (threadIdx.x < kLossWarps) dsum[threadIdx.x] = 0.0;
   for (int i = threadIdx.x; i < kLossWarps * kMaxE; i += kLossThreads) psum[i] = 0.0f;
   __syncthreads();
-  if (lo < hi) loss_rows<L, V, kSoftmax, true, kGrad>(p, counts, 0, b, e_, lo, hi, psum, dsum);
+  if (lo < hi) loss_rows<L, V, kSoftmax, true, kGrad, true>(p, counts, 0, b, e_, lo, hi, psum, dsum);
   for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
     float t = 0.0f;
 #pragma unroll
@@ -490,12 +544,17 @@ LossPlan loss_plan(int64_t N, int32_t E) {
 
 template <bool kProb, bool kGrad>
 struct LossPass {
-  int64_t chunks;
+  int64_t chunks;           // without the counting pass in front of it an ordinary launch, behind a memset
   template <int L, int V>
   cudaError_t run(const LossParams& p, int score, cudaStream_t s) const {
     auto kern = score == KOLIBRI_SCORE_SOFTMAX ? balance_loss_kernel<L, V, true, kProb, kGrad>
                                                : balance_loss_kernel<L, V, false, kProb, kGrad>;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(chunks)), dim3(kLossThreads), 0, s, dim3(0, 0, 0), p);
+    if constexpr (kGrad) {
+      return launch_pdl(kern, dim3(static_cast<unsigned>(chunks)), dim3(kLossThreads), 0, s, dim3(0, 0, 0), p);
+    } else {
+      kern<<<static_cast<unsigned>(chunks), kLossThreads, 0, s>>>(p);
+      return cudaGetLastError();
+    }
   }
 };
 
@@ -543,11 +602,12 @@ cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_
   const LossPlan lp = loss_plan(N, E);
   LossParams p{};
   p.z = z;
+  p.ids = ids;
   p.counts = counts;
   p.grad_loss = grad_loss;
   p.gz = gz;
   p.part = static_cast<float*>(ws);
-  p.dots = reinterpret_cast<double*>(static_cast<char*>(ws) +
+  p.none = reinterpret_cast<double*>(static_cast<char*>(ws) +
                                      round256((static_cast<size_t>(lp.chunks) + S) * E * sizeof(float)));
   p.q = Seqs{seq, N, S};
   p.chunk = lp.chunk;
@@ -561,14 +621,17 @@ cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_
   }
   cudaError_t err = cudaMemsetAsync(counts, 0, sizeof(int32_t) * static_cast<size_t>(S) * E, s);
   if (err != cudaSuccess) return err;
-  seq_count_kernel<<<static_cast<unsigned>(lp.chunks), kLossThreads, 0, s>>>(ids, p.q, E, K, lp.chunk, counts);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
+  if (gz) {
+    seq_count_kernel<<<static_cast<unsigned>(lp.chunks), kLossThreads, 0, s>>>(ids, p.q, E, K, lp.chunk, counts);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
   err = gz ? launch_by_width(LossPass<true, true>{lp.chunks}, p, score, s)
            : launch_by_width(LossPass<true, false>{lp.chunks}, p, score, s);
   if (err != cudaSuccess) return err;
-  return launch_pdl(balance_finish_kernel, dim3(static_cast<unsigned>((E + 31) / 32) * S), dim3(32, kFinishRows), 0, s, dim3(0, 0, 0), p, prob,
-                    loss);
+  const unsigned tiles = static_cast<unsigned>((E + kFinishCols - 1) / kFinishCols);
+  return launch_pdl(balance_finish_kernel, dim3(tiles * static_cast<unsigned>(S)), dim3(32, kFinishRows), 0, s,
+                    dim3(tiles, 1, 1), p, prob, loss);
 }
 
 cudaError_t launch_balance_loss_grad(const float* z, const int32_t* counts, const int64_t* seq, int64_t N,
@@ -577,7 +640,7 @@ cudaError_t launch_balance_loss_grad(const float* z, const int32_t* counts, cons
   const LossPlan lp = loss_plan(N, E);
   LossParams p{};
   p.z = z;
-  p.counts = counts;
+  p.counts = const_cast<int32_t*>(counts);       // read only
   p.grad_loss = grad_loss;
   p.gz = gz;
   p.q = Seqs{seq, N, S};

@@ -137,9 +137,10 @@ def test_padding_is_not_read(score):
 
 
 @pytest.mark.parametrize("score", SCORES)
-def test_extreme_logits(score):
+@pytest.mark.parametrize("N", [64, 1100])
+def test_extreme_logits(score, N):
     """-infinity for some experts and for a whole row, rows far below zero, far above, the type's lowest value."""
-    N, E, K = 64, 128, 4
+    E, K = 128, 4
     z, ids, seq, up = _inputs(N, E, K, [0, N], 5)
     z[:, 5] = -torch.inf
     z[3] = -torch.inf
@@ -151,6 +152,9 @@ def test_extreme_logits(score):
     got = B.kolibri_balance_loss(z, ids, 1.0, seq_offsets=seq, score=score, grad_loss=up, want_gz=True)
     assert torch.isfinite(got[0]).all() and torch.isfinite(got[2]).all() and torch.isfinite(got[3]).all()
     assert not got[3][3].any() and not got[3][:, 5].any()
+    assert ((got[0].double() - want["loss"]).abs() <= 4 * want["lbar"]).all()       # P is held to four times its bar below
+    alone = B.kolibri_balance_loss(z, ids, 1.0, seq_offsets=seq, score=score)
+    assert torch.equal(alone[0], got[0]) and torch.equal(alone[2], got[2])
     # logits of this size enter the exponential unreduced: their rows are held to the units it is then off by
     big = torch.zeros(N, 1, dtype=torch.float64, device="cuda")
     big[[7, 9, 11]] = 1.0
@@ -180,9 +184,10 @@ def test_bad_ids_and_offsets_are_reported():
     check_status()
 
 
-def test_even_loads_have_the_formulas_loss():
+@pytest.mark.parametrize("N", [512, 4096])
+def test_even_loads_have_the_formulas_loss(N):
     """Every expert equally loaded: f = 1, so L = lambda and the gradient vanishes, exactly."""
-    N, E, K = 512, 64, 2
+    E, K = 64, 2
     z = torch.randn(N, E, device="cuda")
     ids = (torch.arange(N * K, device="cuda") % E).view(N, K).to(torch.int32)
     loss, counts, prob, gz = B.kolibri_balance_loss(z, ids, 0.25, want_gz=True)
