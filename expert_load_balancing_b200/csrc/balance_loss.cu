@@ -190,6 +190,9 @@ template <int L, int V, bool kSoftmax, bool kProb, bool kGrad, bool kDots>
 __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* counts, int s, int64_t b, int64_t e_,
                                           int64_t lo, int64_t hi, float* psum, double* dsum) {
   constexpr int kRows = 32 / L;          // rows of a warp at once
+  // The next rows are on their way while these are worked on, where the registers are there for it (65,536 rows of
+  // 128, two blocks per SM: the gradient's pass 13.9 -> 12.4 us, the other 17.1 -> 16.3).
+  constexpr bool kAhead = V == 4;
   const int lane = threadIdx.x & (L - 1), group = (threadIdx.x & 31) / L, warp = threadIdx.x >> 5;
   const int E4 = p.E >> 2;
   // f - 1 = (E c - K T) / (K T), the numerator an integer: exact where loads are even
@@ -212,18 +215,27 @@ __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* co
   if constexpr (kGrad)
     gscale = __fdiv_rn(static_cast<float>(p.lambda) * (p.grad_loss ? p.grad_loss[s] : 1.0f), static_cast<float>(e_ - b));
   double dot_sum = 0.0;
-  for (int64_t base = lo + warp * kRows; base < hi; base += kRows * kLossWarps) {
-    const int64_t row = base + group;
-    const bool there = row < hi;
+  float4 next[V];
+  auto fetch = [&](int64_t row) {
     const float4* zr = reinterpret_cast<const float4*>(p.z) + row * E4;
-    float z[4 * V], u[4 * V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c4 = lane + L * j;
-      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (c4 < E4 && there) v = __ldcs(zr + c4);
-      z[4 * j] = v.x; z[4 * j + 1] = v.y; z[4 * j + 2] = v.z; z[4 * j + 3] = v.w;
+      next[j] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (c4 < E4 && row < hi) next[j] = __ldcs(zr + c4);
     }
+  };
+  if (kAhead) fetch(lo + warp * kRows + group);
+  for (int64_t base = lo + warp * kRows; base < hi; base += kRows * kLossWarps) {
+    const int64_t row = base + group;
+    const bool there = row < hi;
+    if (!kAhead) fetch(row);
+    float z[4 * V], u[4 * V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      z[4 * j] = next[j].x; z[4 * j + 1] = next[j].y; z[4 * j + 2] = next[j].z; z[4 * j + 3] = next[j].w;
+    }
+    if (kAhead) fetch(row + kRows * kLossWarps);
     float m = z[0];
 #pragma unroll
     for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, z[i]);
