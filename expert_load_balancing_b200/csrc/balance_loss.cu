@@ -34,6 +34,7 @@
 // on which c + s never repeats, so the share of a pair is kept in row c + s of
 // the workspace.
 #include "launch.h"
+#include "approx.cuh"
 #include "common.cuh"
 #include "pdl.cuh"
 

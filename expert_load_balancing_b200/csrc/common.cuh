@@ -88,20 +88,6 @@ __device__ __forceinline__ float gate_sigmoid(float z) {
   return __double2float_rn(s);
 }
 
-// 2^x and 1 / x by the hardware's approximations, subnormal results flushed:
-// about 2^-22 relative each.
-constexpr float kLog2e = 1.44269504088896340736f;
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

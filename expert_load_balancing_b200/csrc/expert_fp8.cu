@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "launch.h"
+#include "approx.cuh"
 #include "gemm_pair.cuh"
 #include "pdl.cuh"
 

@@ -25,6 +25,7 @@
 #include <cuda_fp8.h>
 
 #include "launch.h"
+#include "approx.cuh"
 #include "common.cuh"
 #include "pdl.cuh"
 
