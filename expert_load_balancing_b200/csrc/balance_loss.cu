@@ -14,9 +14,9 @@
 // exact to fp32 when the loads are nearly even: dot_t = sum_j (f_j - 1) p_tj,
 // and at even loads L is lambda and the gradient 0 to the last bit.
 //
-// Measured (E = 384, 6 of them chosen, loss and gradient): 1,048,576 rows 576 us,
-// 0.86 of a copy's bandwidth for the 3.25 GB: counts 13, the pass 550, the finish
-// 7, and the gaps.
+// Measured (E = 384, 6 of them chosen, loss and gradient): 1,048,576 rows 564-572
+// us, 0.87 of a copy's bandwidth for the 3.25 GB: counts 13, the pass 540-550, the
+// finish 7.
 //
 // The gradient needs f, which comes from the ids alone, and not P: so with the
 // gradient the counts are formed first (a read of the ids) and ONE pass over Z
