@@ -639,7 +639,7 @@ KOLIBRI_API kolibri_status kolibri_rms_norm_grad(const void *gy, int32_t gy_type
  *       s_down [E, d/128, F/128] fp32
  *   shared expert ws_gate_up [2F, d], ss_gate_up [2F/128, d/128], ws_down
  *       [d, F], ss_down [d/128, F/128], or all four NULL
- *   y [N, d] bf16, written
+ *   y [N, d] bf16, written; y and ws must not overlap one another or the inputs
  * Arithmetic: products of e4m3 values accumulated on the tensor cores over 128
  * values of k, then scaled and summed in fp32.  h = SiLU(g) u in fp32 is held
  * in e4m3 with a scale max(amax |h|, 1e-30) / 448 per 128 units; an expert's

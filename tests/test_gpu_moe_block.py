@@ -229,3 +229,43 @@ def test_memory_of_a_call_on_another_stream(which):
     assert all((c == 5).all() for c in copies)
     assert all(torch.equal(a.view(torch.uint8), w.view(torch.uint8)) for a, w in zip(got, want))
     check_status()
+
+
+def test_two_graphs_with_one_workspace():
+    """Two batches captured apart on the same workspaces, replayed in turn: each leaves its own results."""
+    L = Layer(512, 256, 64, 2, 8)
+    sizes = (700, 90)
+    fws = B.expert_ffn_fp8_workspace(max(sizes), 512, 256, 2, True).fill_(255)
+    pws = [B.workspace(B.KOLIBRI_OP_PERMUTE, n, L.E, L.K) for n in sizes]
+    nbytes = max(max(B.load().kolibri_balance_loss_workspace_size(n, L.E, 1), B.load().kolibri_rms_norm_grad_workspace_size(n, 512))
+                 for n in sizes)
+    lws = torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+    runs = []
+    for n, pw in zip(sizes, pws):
+        x, b = L.rnd(n, 512).to(BF), L.buffers(n)
+        o = dict(loss=torch.zeros(1, device="cuda"), counts=torch.zeros(1, L.E, dtype=torch.int32, device="cuda"),
+                 prob=torch.zeros(1, L.E, device="cuda"), gz=torch.zeros(n, L.E, device="cuda"),
+                 gx=torch.zeros(n, 512, dtype=BF, device="cuda"), gw=torch.zeros(512, device="cuda"))
+
+        def call(x=x, b=b, o=o, pw=pw):
+            L.forward(x, x, pw, fws, b)
+            B.kolibri_balance_loss(b["z"], b["ids"], 0.1, gz=o["gz"], loss=o["loss"], counts=o["counts"], prob=o["prob"],
+                                   ws=lws)
+            B.kolibri_rms_norm_grad(b["y"], b["res"], L.norm, EPS, gx=o["gx"], gweight=o["gw"], ws=lws)
+
+        call()
+        torch.cuda.synchronize()
+        out = [b["ffn"], *o.values()]
+        want = [t.clone() for t in out]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        for t in out:
+            t.fill_(1)
+        runs.append((graph, out, want, call))          # call holds the arrays that the graph reads
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        runs[i][0].replay()
+    torch.cuda.synchronize()
+    for _, out, want, _ in runs:
+        assert all(torch.equal(a, w) for a, w in zip(out, want))
+    check_status()
