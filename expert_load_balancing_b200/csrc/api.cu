@@ -452,13 +452,14 @@ kolibri_status kolibri_balance_loss(const float* z, const int32_t* ids, const in
                                     float* prob, float* gz, void* ws, size_t ws_bytes, void* stream) {
   const kolibri_status st = check_balance_loss(N, E, K, S, seq_offsets, score, accumulate, lambda);
   if (st != KOLIBRI_OK) return st;
-  if (!z || !ids || !loss || !counts || !prob || !ws) return KOLIBRI_ERR_INVALID_ARG;
+  const size_t need = balance_loss_ws_bytes(N, E, S);
+  if (!z || !ids || !loss || !counts || !prob || (need && !ws)) return KOLIBRI_ERR_INVALID_ARG;
   for (const void* q : {static_cast<const void*>(z), static_cast<const void*>(ids),
                         static_cast<const void*>(seq_offsets), static_cast<const void*>(grad_loss),
                         static_cast<const void*>(loss), static_cast<const void*>(counts),
                         static_cast<const void*>(prob), static_cast<const void*>(gz), static_cast<const void*>(ws)})
     if (!aligned16(q)) return KOLIBRI_ERR_INVALID_ARG;
-  if (ws_bytes < balance_loss_ws_bytes(N, E, S)) return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < need) return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
   return from_cuda(launch_balance_loss(z, ids, seq_offsets, N, E, K, S, score, lambda, grad_loss, accumulate, loss,
                                        counts, prob, gz, ws, static_cast<cudaStream_t>(stream)));
 }

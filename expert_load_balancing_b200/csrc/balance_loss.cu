@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(32 * kFinishRows) balance_finish_kernel(const 
 // reads at most 128 rows (E = 384: 197 KB, about 2 us).
 constexpr int kClusterBlocks = 8;
 constexpr int64_t kSmallRows = 1024;
+bool small_batch(int64_t N, int32_t S) { return S == 1 && N <= kSmallRows; }
 
 template <int L, int V, bool kSoftmax, bool kGrad>
 __global__ void __launch_bounds__(kLossThreads) balance_small_kernel(const LossParams p, const int32_t* ids,
@@ -604,6 +605,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 size_t balance_loss_ws_bytes(int64_t N, int32_t E, int32_t S) {
+  if (small_batch(N, S)) return 0;
   const size_t rows = static_cast<size_t>(loss_plan(N, E).chunks) + S;
   return round256(rows * E * sizeof(float)) + rows * sizeof(double);
 }
@@ -628,7 +630,7 @@ cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_
   p.K = K;
   p.accumulate = accumulate;
   p.lambda = lambda;
-  if (S == 1 && N <= kSmallRows) {
+  if (small_batch(N, S)) {
     p.chunk = (N + kClusterBlocks - 1) / kClusterBlocks;
     return launch_by_width(SmallPass{ids, counts, prob, loss}, p, score, s);
   }

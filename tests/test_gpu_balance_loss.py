@@ -225,7 +225,7 @@ def test_refusals():
     with pytest.raises(B.KolibriError):
         B.kolibri_balance_loss(z, ids, float("nan"))
     with pytest.raises(B.KolibriError):
-        B.kolibri_balance_loss(z, ids, 1e-3, ws=torch.empty(64, device="cuda", dtype=torch.uint8))
+        B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq, ws=torch.empty(64, device="cuda", dtype=torch.uint8))
     with pytest.raises(ValueError):
         B.kolibri_balance_loss_grad(z, ids, 4, 1e-3)
 

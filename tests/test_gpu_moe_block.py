@@ -192,7 +192,7 @@ def test_memory_of_a_call_on_another_stream(which):
     """A call on a busy stream that allocates what it needs.  What the current stream allocates meanwhile is not the
     call's workspace, and memory that the current stream has still to read is not given to the call."""
     L = Layer(512, 256, 64, 2, 6)
-    N = 900
+    N = 1100                                  # the loss has a workspace from 1025 rows on
     x = L.rnd(N, 512).to(BF)
     b = L.buffers(N)
     L.forward(x, x, B.workspace(B.KOLIBRI_OP_PERMUTE, N, L.E, L.K), B.expert_ffn_fp8_workspace(N, 512, 256, 2, True), b)
