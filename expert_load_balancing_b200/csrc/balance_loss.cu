@@ -44,6 +44,8 @@ namespace {
 
 constexpr int kLossWarps = 8;
 constexpr int kLossThreads = 32 * kLossWarps;
+constexpr int kSmallWarps = 16;          // of the small form, whose eight blocks have an SM each
+constexpr int kSmallThreads = 32 * kSmallWarps;
 constexpr int kCountAhead = 8;           // ids in flight per thread of the counting pass
 constexpr int kMaxE = KOLIBRI_MAX_EXPERTS;
 
@@ -90,16 +92,17 @@ __device__ __forceinline__ void check_seqs(const Seqs& q) {
 }
 
 // hist[e] += the slots of the rows [lo, hi) that are routed to e.
+template <int kThreads>
 __device__ __forceinline__ void count_rows(const int32_t* ids, int64_t lo, int64_t hi, int E, int K, int32_t* hist) {
   const int64_t j1 = hi * K;
-  for (int64_t j = lo * K + threadIdx.x; j < j1; j += kCountAhead * kLossThreads) {
+  for (int64_t j = lo * K + threadIdx.x; j < j1; j += kCountAhead * kThreads) {
     int32_t e[kCountAhead];
 #pragma unroll
     for (int i = 0; i < kCountAhead; ++i)
-      if (j + i * kLossThreads < j1) e[i] = __ldcs(ids + j + i * kLossThreads);
+      if (j + i * kThreads < j1) e[i] = __ldcs(ids + j + i * kThreads);
 #pragma unroll
     for (int i = 0; i < kCountAhead; ++i)
-      if (j + i * kLossThreads < j1) {
+      if (j + i * kThreads < j1) {
         if (e[i] >= 0 && e[i] < E) atomicAdd(&hist[e[i]], 1);
         else raise_status(kStatusBadInput);
       }
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(kLossThreads) seq_count_kernel(const int32_t* 
     if (b >= r1) break;
     const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
     if (lo >= hi) continue;
-    count_rows(ids, lo, hi, E, K, hist);
+    count_rows<kLossThreads>(ids, lo, hi, E, K, hist);
     __syncthreads();
     flush_counts(hist, E, counts + static_cast<int64_t>(s) * E);
     __syncthreads();
@@ -191,6 +194,7 @@ template <int L, int V, bool kSoftmax, bool kProb, bool kGrad, bool kDots>
 __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* counts, int s, int64_t b, int64_t e_,
                                           int64_t lo, int64_t hi, float* psum, double* dsum) {
   constexpr int kRows = 32 / L;          // rows of a warp at once
+  constexpr int kWarps = kDots ? kSmallWarps : kLossWarps;
   // The next rows are on their way while these are worked on, where the registers are there for it (65,536 rows of
   // 128, two blocks per SM: the gradient's pass 13.9 -> 12.4 us, the other 17.1 -> 16.3).
   constexpr bool kAhead = V == 4;
@@ -227,7 +231,7 @@ __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* co
     }
   };
   if (kAhead) fetch(lo + warp * kRows + group);
-  for (int64_t base = lo + warp * kRows; base < hi; base += kRows * kLossWarps) {
+  for (int64_t base = lo + warp * kRows; base < hi; base += kRows * kWarps) {
     const int64_t row = base + group;
     const bool there = row < hi;
     if (!kAhead) fetch(row);
@@ -236,7 +240,7 @@ __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* co
     for (int j = 0; j < V; ++j) {
       z[4 * j] = next[j].x; z[4 * j + 1] = next[j].y; z[4 * j + 2] = next[j].z; z[4 * j + 3] = next[j].w;
     }
-    if (kAhead) fetch(row + kRows * kLossWarps);
+    if (kAhead) fetch(row + kRows * kWarps);
     float m = z[0];
 #pragma unroll
     for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, z[i]);
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_l
     const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
     if (lo >= hi) continue;
     int32_t* const counts = p.counts + static_cast<int64_t>(s) * p.E;
-    if constexpr (kCount) count_rows(p.ids, lo, hi, p.E, p.K, hist);
+    if constexpr (kCount) count_rows<kLossThreads>(p.ids, lo, hi, p.E, p.K, hist);
     loss_rows<L, V, kSoftmax, kProb, kGrad, false>(p, counts, s, b, e_, lo, hi, psum, dsum);
     if constexpr (kCount) flush_counts(hist, p.E, counts);
     if constexpr (kProb) {
@@ -461,26 +465,31 @@ __global__ void __launch_bounds__(32 * kFinishRows) balance_finish_kernel(const 
 
 // A small batch of one sequence: one launch, a cluster of eight blocks that
 // hold the counts and the shares of P in shared memory and read one another's.
-// The four launches of the other form cost 12 us whatever the size; 256 rows of
-// 384 take 10.3 (in a graph), most of it the three cluster barriers and the
-// chains from ids to counts to loss.  Up to 1024 rows: each of the eight SMs then
-// reads at most 128 rows (E = 384: 197 KB, about 2 us).
+// The launches of the other form cost 12.3 us whatever the size; 256 rows of 384
+// take 7.2 here (9.0 with eight warps), 64 rows 5.6 (in a graph).  Eight SMs
+// cannot carry more: 680 rows of 384 12.5 (14.4 the other way), 1024 16.4 (13.5);
+// 512 rows of 512 12.0 (14.1), 1024 of 256 12.3 (12.4).
 constexpr int kClusterBlocks = 8;
 constexpr int64_t kSmallRows = 1024;
-bool small_batch(int64_t N, int32_t S) { return S == 1 && N <= kSmallRows; }
+constexpr int64_t kSmallLogits = 1 << 18;
+// Up to this many slots each block counts all ids: one round of loads in place of
+// a barrier of the cluster and a round of remote ones (64 rows of 384, K = 6, eight
+// warps: 5.1 us, 6.0 with the barrier; 680 rows: 15.6 and 15.8).
+constexpr int64_t kAloneSlots = 4096;
+bool small_batch(int64_t N, int32_t E, int32_t S) { return S == 1 && N <= kSmallRows && N * E <= kSmallLogits; }
 
 template <int L, int V, bool kSoftmax, bool kGrad>
-__global__ void __launch_bounds__(kLossThreads) balance_small_kernel(const LossParams p, const int32_t* ids,
+__global__ void __launch_bounds__(kSmallThreads) balance_small_kernel(const LossParams p, const int32_t* ids,
                                                                      int32_t* counts_out, float* prob, float* loss) {
-  __shared__ float psum[kLossWarps * kMaxE];
-  __shared__ double dsum[kLossWarps];
+  __shared__ float psum[kSmallWarps * kMaxE];
+  __shared__ double dsum[kSmallWarps];
   __shared__ int32_t hist[kMaxE];
   __shared__ __align__(16) int32_t counts[kMaxE];
   __shared__ float share[kMaxE];
   __shared__ double dots;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  for (int e = threadIdx.x; e < p.E; e += kLossThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < p.E; e += kSmallThreads) hist[e] = 0;
   pdl_wait();
   const Seqs q = p.q;
   if (rank == 0 && threadIdx.x == 0 && q.seq && (q.seq[0] < 0 || q.seq[0] > q.seq[1] || q.seq[1] > q.N))
@@ -489,44 +498,53 @@ __global__ void __launch_bounds__(kLossThreads) balance_small_kernel(const LossP
   const int64_t r0 = rank * p.chunk, r1 = r0 + p.chunk < q.N ? r0 + p.chunk : q.N;
   const int64_t lo = b > r0 ? b : r0, hi = e_ < r1 ? e_ : r1;
   __syncthreads();
-  for (int64_t j = lo * p.K + threadIdx.x; j < hi * p.K; j += kLossThreads) {
-    const int32_t e = ids[j];
-    if (e >= 0 && e < p.E) atomicAdd(&hist[e], 1);
-    else raise_status(kStatusBadInput);
+  const bool alone = (e_ - b) * p.K <= kAloneSlots;
+  if (alone) {
+    count_rows<kSmallThreads>(ids, b, e_, p.E, p.K, hist);
+    __syncthreads();
+  } else {
+    count_rows<kSmallThreads>(ids, lo, hi, p.E, p.K, hist);
+    cluster_barrier();
   }
-  cluster_barrier();
-  for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
+  for (int e = threadIdx.x; e < p.E; e += kSmallThreads) {
     int32_t c = 0;
+    if (alone) {
+      c = hist[e];
+    } else {
 #pragma unroll
-    for (uint32_t r = 0; r < kClusterBlocks; ++r) c += static_cast<int32_t>(remote_u32(hist + e, r));
+      for (uint32_t r = 0; r < kClusterBlocks; ++r) c += static_cast<int32_t>(remote_u32(hist + e, r));
+    }
     counts[e] = c;
     if (rank == 0) counts_out[e] = c;
   }
   __syncthreads();
   if constexpr (kGrad) {
     if (!p.accumulate)
-      for (int64_t i = r0 * p.E + threadIdx.x; i < r1 * p.E; i += kLossThreads)
+      for (int64_t i = r0 * p.E + threadIdx.x; i < r1 * p.E; i += kSmallThreads)
         if (i < b * p.E || i >= e_ * p.E) p.gz[i] = 0.0f;
   }
-  if (threadIdx.x < kLossWarps) dsum[threadIdx.x] = 0.0;
-  for (int i = threadIdx.x; i < kLossWarps * kMaxE; i += kLossThreads) psum[i] = 0.0f;
-  __syncthreads();
-  if (lo < hi) loss_rows<L, V, kSoftmax, true, kGrad, true>(p, counts, 0, b, e_, lo, hi, psum, dsum);
-  for (int e = threadIdx.x; e < p.E; e += kLossThreads) {
+  if (lo < hi) {
+    loss_rows<L, V, kSoftmax, true, kGrad, true>(p, counts, 0, b, e_, lo, hi, psum, dsum);
+  } else {
+    if (threadIdx.x < kSmallWarps) dsum[threadIdx.x] = 0.0;
+    for (int i = threadIdx.x; i < kSmallWarps * kMaxE; i += kSmallThreads) psum[i] = 0.0f;
+    __syncthreads();
+  }
+  for (int e = threadIdx.x; e < p.E; e += kSmallThreads) {
     float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kLossWarps; ++w) t += psum[w * kMaxE + e];
+    for (int w = 0; w < kSmallWarps; ++w) t += psum[w * kMaxE + e];
     share[e] = t;
   }
   if (threadIdx.x == 0) {
     double t = 0.0;
 #pragma unroll
-    for (int w = 0; w < kLossWarps; ++w) t += dsum[w];
+    for (int w = 0; w < kSmallWarps; ++w) t += dsum[w];
     dots = t;
   }
   cluster_barrier();
   const int64_t n = e_ - b;
-  for (int e = rank * kLossThreads + threadIdx.x; e < p.E; e += kClusterBlocks * kLossThreads) {
+  for (int e = rank * kSmallThreads + threadIdx.x; e < p.E; e += kClusterBlocks * kSmallThreads) {
     double t = 0.0;
 #pragma unroll
     for (uint32_t r = 0; r < kClusterBlocks; ++r) t += __uint_as_float(remote_u32(share + e, r));
@@ -580,7 +598,7 @@ struct SmallPass {
   template <int L, int V, bool kSoftmax>
   cudaError_t launch(const LossParams& p, cudaStream_t s) const {
     auto kern = p.gz ? balance_small_kernel<L, V, kSoftmax, true> : balance_small_kernel<L, V, kSoftmax, false>;
-    return launch_pdl(kern, dim3(kClusterBlocks), dim3(kLossThreads), 0, s, dim3(kClusterBlocks, 1, 1), p, ids, counts,
+    return launch_pdl(kern, dim3(kClusterBlocks), dim3(kSmallThreads), 0, s, dim3(kClusterBlocks, 1, 1), p, ids, counts,
                       prob, loss);
   }
   template <int L, int V>
@@ -605,7 +623,7 @@ size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 size_t balance_loss_ws_bytes(int64_t N, int32_t E, int32_t S) {
-  if (small_batch(N, S)) return 0;
+  if (small_batch(N, E, S)) return 0;
   const size_t rows = static_cast<size_t>(loss_plan(N, E).chunks) + S;
   return round256(rows * E * sizeof(float)) + rows * sizeof(double);
 }
@@ -630,7 +648,7 @@ cudaError_t launch_balance_loss(const float* z, const int32_t* ids, const int64_
   p.K = K;
   p.accumulate = accumulate;
   p.lambda = lambda;
-  if (small_batch(N, S)) {
+  if (small_batch(N, E, S)) {
     p.chunk = (N + kClusterBlocks - 1) / kClusterBlocks;
     return launch_by_width(SmallPass{ids, counts, prob, loss}, p, score, s);
   }

@@ -556,7 +556,7 @@ KOLIBRI_API kolibri_status kolibri_expert_combine(const float *y_perm, const flo
  *   gz          [N, E] fp32, or NULL: no gradient
  *   ws          kolibri_balance_loss_workspace_size(N, E, S) bytes, 16-byte
  *               aligned; need not be initialised; may be NULL where that is 0
- *               (one sequence of up to 1024 rows)
+ *               (one sequence, N <= 1024 and N E <= 2^18)
  * Outputs must not overlap one another, the inputs or ws.
  * 1 <= K < E <= 512, K <= 16, E % 4 == 0, S E < 2^31.  Sums over tokens do not
  * depend on the order in which blocks run: the same inputs give the same bits

@@ -82,6 +82,9 @@ def _inputs(N, E, K, cut, seed, spread=1.5):
 
 
 CASES = [
+    # either side of the small form, with few slots and with many
+    (682, 384, 6, [0, 682]), (683, 384, 6, [0, 683]), (683, 384, 5, [3, 680]), (512, 512, 9, [0, 512]), (512, 512, 3, [20, 500]),
+    (1024, 256, 16, [0, 1024]), (1024, 256, 4, [1, 1024]), (1024, 256, 3, [700, 1024]),
     (1, 4, 1, [0, 1]), (1024, 384, 6, [0, 1024]), (1024, 512, 3, [100, 900]), (1025, 384, 6, [0, 1025]), (1000, 64, 8, [0, 0]), (513, 200, 2, [7, 513]), (900, 128, 4, [0, 3]), (1, 384, 6, [0, 1]), (2, 8, 3, [0, 1, 2]), (5, 132, 8, [0, 0, 5, 5]), (7, 128, 8, [0, 7]),
     (256, 384, 6, [0, 256]), (257, 260, 2, [0, 100, 100, 257]), (1000, 512, 16, [0, 1, 2, 3, 500, 1000]),
     (4096, 384, 6, [0, 4096]), (5003, 128, 8, [0, 17, 4000, 4000, 4001, 5003]), (700, 64, 1, list(range(0, 701))),

@@ -61,7 +61,8 @@ def test_balance_loss_checks(lib):
     n, E, K, S = 4096, 384, 6, 5
     need = size(n, E, S)
     assert need >= 4 * E * (S + 1)
-    assert size(1024, E, 1) == 0 and size(1025, E, 1) > 0 and size(1024, E, 2) > 0      # a small batch needs none
+    assert size(682, E, 1) == 0 and size(683, E, 1) > 0 and size(682, E, 2) > 0      # a small batch needs none
+    assert size(1024, 64, 1) == 0 and size(1025, 64, 1) > 0
     assert size(0, E, S) == 0 and size(n, 0, S) == 0 and size(n, 513, S) == 0 and size(n, E, 0) == 0
     f = lib.kolibri_balance_loss
     #        z  ids seq N  E  K  S  score lambda gl acc loss counts prob gz ws ws_bytes stream
