@@ -23,12 +23,15 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; }
 
+// N * per < limit (per >= 1) for any N: the product itself may leave 64 bits.
+bool rows_below(int64_t N, int64_t per, int64_t limit) { return N <= (limit - 1) / per; }
+
 kolibri_status check_ek(int64_t N, int32_t E, int32_t K) {
   if (N < 1 || E < 1 || K < 1) return KOLIBRI_ERR_INVALID_ARG;
   if (K >= E) return KOLIBRI_ERR_INVALID_ARG;
   if (E > KOLIBRI_MAX_EXPERTS || K > KOLIBRI_MAX_TOPK || (E % 4) != 0)
     return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
-  if (N * static_cast<int64_t>(K) >= (static_cast<int64_t>(1) << 31))
+  if (!rows_below(N, K, static_cast<int64_t>(1) << 31))
     return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
   return KOLIBRI_OK;
 }
@@ -352,7 +355,7 @@ constexpr int64_t kExpertRowLimit = (static_cast<int64_t>(1) << 31) - 512;
 
 size_t kolibri_expert_ffn_workspace_size(int64_t N, int32_t d, int32_t F, int32_t K,
                                          int32_t shared) {
-  if (N < 1 || K < 1 || d < 1 || F < 1) return 0;
+  if (N < 1 || K < 1 || d < 1 || F < 1 || !rows_below(N, K, kExpertRowLimit)) return 0;
   return expert_layout(N, d, F, K, shared != 0).total;
 }
 
@@ -368,7 +371,7 @@ kolibri_status kolibri_expert_ffn(const void* x, const int32_t* perm, const int6
       !aligned16(ws) || (ws_gate_up && (!aligned16(ws_gate_up) || !aligned16(ws_down))))
     return KOLIBRI_ERR_INVALID_ARG;
   if (N < 1 || K < 1 || K > 32 || K > E) return KOLIBRI_ERR_INVALID_ARG;
-  if (!expert_shape_supported(d, F, E) || N * K >= kExpertRowLimit) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
+  if (!expert_shape_supported(d, F, E) || !rows_below(N, K, kExpertRowLimit)) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < expert_layout(N, d, F, K, ws_gate_up != nullptr).total)
     return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
   return from_cuda(launch_expert_ffn(x, perm, offsets, inv, gates, w_gate_up, w_down, ws_gate_up,
@@ -379,7 +382,7 @@ kolibri_status kolibri_expert_dispatch(const void* x, const int32_t* perm, int64
                                        int32_t K, void* x_perm, void* stream) {
   if (!x || !perm || !x_perm || !aligned16(x) || !aligned16(x_perm)) return KOLIBRI_ERR_INVALID_ARG;
   if (N < 1 || K < 1 || d < 1) return KOLIBRI_ERR_INVALID_ARG;
-  if (d % 8 != 0 || d > 8192 || N * K >= kExpertRowLimit) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
+  if (d % 8 != 0 || d > 8192 || !rows_below(N, K, kExpertRowLimit)) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
   return from_cuda(launch_expert_dispatch(x, perm, N, d, K, x_perm, static_cast<cudaStream_t>(stream)));
 }
 
@@ -411,7 +414,7 @@ kolibri_status kolibri_expert_combine(const float* y_perm, const float* y_shared
       (y_shared && !aligned16(y_shared)))
     return KOLIBRI_ERR_INVALID_ARG;
   if (N < 1 || K < 1 || K > 32 || d < 4) return KOLIBRI_ERR_INVALID_ARG;
-  if (d % 4 != 0 || N * K >= kExpertRowLimit) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
+  if (d % 4 != 0 || !rows_below(N, K, kExpertRowLimit)) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
   return from_cuda(launch_expert_combine(y_perm, y_shared, inv, gates, N, d, K, y,
                                          static_cast<cudaStream_t>(stream)));
 }
@@ -440,7 +443,7 @@ kolibri_status check_norm(int64_t N, int32_t d, float eps) {
 }  // namespace
 
 size_t kolibri_balance_loss_workspace_size(int64_t N, int32_t E, int32_t S) {
-  if (N < 1 || E < 1 || E > KOLIBRI_MAX_EXPERTS || S < 1 ||
+  if (N < 1 || N >= (static_cast<int64_t>(1) << 31) || E < 1 || E > KOLIBRI_MAX_EXPERTS || S < 1 ||
       static_cast<int64_t>(S) * E >= (static_cast<int64_t>(1) << 31))
     return 0;
   return balance_loss_ws_bytes(N, E, S);
@@ -512,7 +515,7 @@ kolibri_status kolibri_rms_norm_grad(const void* gy, int32_t gy_type, const void
 }
 
 size_t kolibri_expert_ffn_fp8_workspace_size(int64_t N, int32_t d, int32_t F, int32_t K, int32_t shared) {
-  if (N < 1 || K < 1 || K > KOLIBRI_MAX_TOPK || N * (K + 1) >= kExpertRowLimit || !expert_fp8_shape_supported(d, F, 1))
+  if (N < 1 || K < 1 || K > KOLIBRI_MAX_TOPK || !rows_below(N, K + 1, kExpertRowLimit) || !expert_fp8_shape_supported(d, F, 1))
     return 0;
   return expert_fp8_ws_bytes(N, d, F, K, shared != 0);
 }
@@ -536,7 +539,7 @@ kolibri_status kolibri_expert_ffn_fp8(const void* x8, const float* x_scale, cons
                         static_cast<const void*>(ss_down), static_cast<const void*>(y), static_cast<const void*>(ws)})
     if (!aligned16(q)) return KOLIBRI_ERR_INVALID_ARG;
   if (N < 1 || K < 1 || K > KOLIBRI_MAX_TOPK || E < 1 || d < 1 || F < 1) return KOLIBRI_ERR_INVALID_ARG;
-  if (!expert_fp8_shape_supported(d, F, E) || N * (K + 1) >= kExpertRowLimit) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
+  if (!expert_fp8_shape_supported(d, F, E) || !rows_below(N, K + 1, kExpertRowLimit)) return KOLIBRI_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < expert_fp8_ws_bytes(N, d, F, K, shared)) return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
   const ExpertFp8Args a{x8, x_scale, perm, offsets, inv, gates, w_gate_up, s_gate_up, w_down, s_down, ws_gate_up,
                         ss_gate_up, ws_down, ss_down, y, N, d, F, E, K, ws};

@@ -132,3 +132,20 @@ def test_expert_fp8_checks(lib):
     assert call(n=0) == INVALID and call(K=0) == INVALID and call(K=17) == INVALID and call(E=0) == INVALID
     assert call(d=2432) == SHAPE and call(Fh=192) == SHAPE and call(E=513) == SHAPE and call(d=8448) == SHAPE
     assert call(n=1 << 29) == SHAPE
+
+
+def test_row_counts_whose_products_leave_64_bits_are_refused(lib):
+    """N K and N (K + 1) of such an N wrap round to a few rows: the call has to look at N first."""
+    d, Fh, E = 2560, 512, 384
+    for n, K in (((1 << 60) + 1, 15), ((1 << 59) + 1, 16), ((1 << 62) + 1, 3), ((1 << 62) + 1, 4), ((1 << 61) + 3, 8)):
+        assert lib.kolibri_expert_ffn_fp8_workspace_size(n, d, Fh, K, 1) == 0, (n, K)
+        assert lib.kolibri_expert_ffn_fp8(*[F] * 15, n, d, Fh, E, K, F, 1 << 62, None) == SHAPE, (n, K)
+        assert lib.kolibri_balance_loss(F, F, None, n, E, K, 1, 0, 1e-3, None, 0, F, F, F, None, F, 1 << 62, None) == SHAPE, (n, K)
+        assert lib.kolibri_balance_loss_grad(F, F, None, n, E, K, 1, 0, 1e-3, None, 0, F, None) == SHAPE, (n, K)
+        assert lib.kolibri_workspace_bytes(1, n, E, K) == 0, (n, K)
+        assert lib.kolibri_router_topk(F, F, n, E, K, F, F, F, None) == SHAPE, (n, K)
+        assert lib.kolibri_expert_ffn(*[F] * 10, n, d, Fh, E, K, F, 1 << 62, None) == SHAPE, (n, K)
+        assert lib.kolibri_expert_dispatch(F, F, n, d, K, F, None) == SHAPE, (n, K)
+        assert lib.kolibri_expert_combine(F, F, F, F, n, d, K, F, None) == SHAPE, (n, K)
+    for n in (1 << 31, 1 << 62, (1 << 63) - 1):
+        assert lib.kolibri_balance_loss_workspace_size(n, E, 1) == 0 and lib.kolibri_balance_loss_workspace_size(n, E, 2) == 0
