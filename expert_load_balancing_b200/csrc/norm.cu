@@ -219,9 +219,11 @@ __global__ void __launch_bounds__(C == 1 ? 512 : kMaxNormThreads) rms_norm_kerne
 
 // ---- gradient -------------------------------------------------------------
 //
-//   xh = h r, t = gy g:   gx = r (t - xh mean(t xh)) + gres
-//                            = r t - h r^3 (sum t h) / d + gres
+//   xh = h r, t = gy g:   gx = r (t - xh m) + gres,   m = mean(t xh) = r (sum t h) / d
 //   gg = sum over rows of gy xh
+//
+// xh and m stay near 1 and |t| whatever the size of h; r^3, in h r^3 (sum t h) / d, leaves fp32's
+// range for |h| above 1e13 and, where eps allows it, below 1e-13.
 //
 // Both row sums (h^2 and t h) are reduced together; the block's share of gg
 // stays in registers over its rows and goes to one row of the workspace, and
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1) rms_norm_gr
     }
     block_sums<2>(s, buf[flip], warps);
     const float r = rsqrtf(fmaf(s[0], p.inv_d, p.eps));
-    const float k = r * r * r * (s[1] * p.inv_d);
+    const float m = r * (s[1] * p.inv_d);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int v = threadIdx.x + c * T;
@@ -310,8 +312,9 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1) rms_norm_gr
         Vec8 o;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
-          gg[c].v[i] = fmaf(tv.v[i], hv.v[i] * r, gg[c].v[i]);
-          o.v[i] = fmaf(tv.v[i] * g[c].v[i], r, -hv.v[i] * k);
+          const float xh = hv.v[i] * r;
+          gg[c].v[i] = fmaf(tv.v[i], xh, gg[c].v[i]);
+          o.v[i] = fmaf(-xh, m, tv.v[i] * g[c].v[i]) * r;
         }
         if constexpr (kRes) {
           const Vec8 av = widen<HT>(a[c]);

@@ -211,6 +211,29 @@ def test_gradient(N, d, ht, gt, wt, gres):
     assert torch.equal(h1, B.kolibri_rms_norm_grad(gy, h, w, EPS)[0])
 
 
+@pytest.mark.parametrize("scale", [1e-18, 1e-3, 1e3, 1e15])
+@pytest.mark.parametrize("N,d,ht,gt,gres", [(37, 2560, FP, FP, False), (37, 2560, BF, BF, True), (1500, 2560, FP, BF, True), (9, 16384, FP, FP, False)])
+def test_gradient_of_small_and_large_values(N, d, ht, gt, gres, scale):
+    """The scales of the forward's test: gx is about gy / |h|, and both of its terms are of that size."""
+    h, _, w = _inputs(N, d, FP, None, BF, 31 + N)
+    h = (h * scale).to(ht)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    gy = _randn(g, N, d, dtype=gt)
+    gr = _randn(g, N, d, dtype=ht, scale=1 / scale) if gres else None
+    gx, gg = B.kolibri_rms_norm_grad(gy, h, w, 0.0, gres=gr)
+    _check_grad(gy, h, w, 0.0, gr, gx, gg)
+
+
+@pytest.mark.parametrize("N", [5, 1500])
+def test_gradient_of_zero_rows_with_a_tiny_eps(N):
+    """h = 0: gx = gy weight / sqrt(eps), and nothing for the weight's gradient."""
+    h, _, w = _inputs(N, 512, FP, None, BF, 41)
+    h[3] = 0.0
+    gy = _randn(torch.Generator(device="cuda").manual_seed(2), N, 512)
+    gx, gg = B.kolibri_rms_norm_grad(gy, h, w, 1e-30)
+    _check_grad(gy, h, w, 1e-30, None, gx, gg)
+
+
 def test_gradient_against_differences():
     """L = sum y c: <gx, v> and <gweight, u> against central differences of the formula in 64 bits."""
     h, _, w = _inputs(6, 264, FP, None, FP, 2)
