@@ -82,10 +82,10 @@ struct Seqs {
   }
 };
 
-// Offsets that decrease or leave [0, N] are reported (block 0).
+// Offsets that decrease or leave [0, N] are reported (the blocks share them).
 __device__ __forceinline__ void check_seqs(const Seqs& q) {
-  if (blockIdx.x == 0 && q.seq)
-    for (int s = threadIdx.x; s <= q.S; s += kLossThreads) {
+  if (q.seq)
+    for (int64_t s = blockIdx.x * kLossThreads + threadIdx.x; s <= q.S; s += static_cast<int64_t>(gridDim.x) * kLossThreads) {
       const int64_t v = q.seq[s];
       if (v < 0 || v > q.N || (s > 0 && q.seq[s - 1] > v)) raise_status(kStatusBadInput);
     }
@@ -335,8 +335,8 @@ __global__ void __launch_bounds__(kLossThreads, LossBlocks<V>::kPerSm) balance_l
   const int64_t r1 = r0 + p.chunk < p.q.N ? r0 + p.chunk : p.q.N;
   pdl_wait();          // the counts
   const Seqs q = p.q.cached(seq_s);
+  if constexpr (kCount || !kProb) check_seqs(q);       // the other form's counting pass has checked them
   if constexpr (kCount) {
-    check_seqs(q);
     for (int e = threadIdx.x; e < p.E; e += kLossThreads) hist[e] = 0;
     __syncthreads();
   }

@@ -187,6 +187,31 @@ def test_bad_ids_and_offsets_are_reported():
     check_status()
 
 
+@pytest.mark.parametrize("score", SCORES)
+def test_gradient_reports_bad_offsets(score):
+    """The gradient alone checks its boundaries as the loss does, in whichever part of them the fault is."""
+    N, E, K = 300, 64, 4
+    z, ids, seq, up = _inputs(N, E, K, [0, 100, N], 6)
+    counts = B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq)[1]
+    B.kolibri_balance_loss_grad(z, counts, K, 1e-3, seq_offsets=seq, score=score)
+    check_status()
+    for cut in ([0, 200, 100], [-5, 100, N], [0, 100, N + 1], [300, 0, 300], [0, N + 1], [200, 100], [-1, N]):
+        S = len(cut) - 1
+        B.kolibri_balance_loss_grad(z, counts[:1].expand(S, E).contiguous(), K, 1e-3, seq_offsets=torch.tensor(cut, device="cuda"), score=score)
+        assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, cut
+    # more boundaries than a block keeps, the fault behind them
+    many = torch.arange(5001, device="cuda").clamp(max=N)
+    one = torch.ones(5000, E, device="cuda", dtype=torch.int32)
+    B.kolibri_balance_loss_grad(z, one, K, 1e-3, seq_offsets=many, score=score)
+    check_status()
+    for at, v in ((0, -1), (2500, N - 1), (4999, 0), (5000, N + 1)):
+        bad = many.clone()
+        bad[at] = v
+        B.kolibri_balance_loss_grad(z, one, K, 1e-3, seq_offsets=bad, score=score)
+        assert B.kolibri_device_status() == B.KOLIBRI_ERR_DEVICE, (at, v)
+    check_status()
+
+
 @pytest.mark.parametrize("N", [512, 4096])
 def test_even_loads_have_the_formulas_loss(N):
     """Every expert equally loaded: f = 1, so L = lambda and the gradient vanishes, exactly."""
