@@ -246,14 +246,14 @@ __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* co
     for (int i = 1; i < 4 * V; ++i) m = fmaxf(m, z[i]);
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const bool none = m == -INFINITY;               // a row behind the last one is such a row too
+    const bool low = m == -INFINITY;
     float sum = 0.0f, dot = 0.0f, ec = 1.0f;
     if constexpr (kSoftmax) {
-      const float c = none ? 0.0f : m;
+      const float c = low ? 0.0f : m;
 #pragma unroll
       for (int i = 0; i < 4 * V; ++i) z[i] = exp2_fast((z[i] - c) * kLog2e);
     } else {
-      const float c = none ? 0.0f : fminf(m, 0.0f);
+      const float c = low ? 0.0f : fminf(m, 0.0f);
       ec = exp2_fast(c * kLog2e);
 #pragma unroll
       for (int i = 0; i < 4 * V; ++i) {
@@ -271,6 +271,9 @@ __device__ __forceinline__ void loss_rows(const LossParams& p, const int32_t* co
       sum += __shfl_xor_sync(0xffffffffu, sum, o);
       dot += __shfl_xor_sync(0xffffffffu, dot, o);
     }
+    // A row of -infinity throughout, as a row behind the last one is.  The score at the maximum is 1/2 at least, so no
+    // other sum is 0.  The maximum does not tell: it passes over NaN, and a row of NaN has to show in P and L.
+    const bool none = sum == 0.0f;
     const float inv = none ? 0.0f : rcp_fast(sum);
     dot = __fmul_rn(dot, inv);          // uncontracted: the same bits in every form of the pass
     if constexpr (kProb) {

@@ -536,7 +536,9 @@ KOLIBRI_API kolibri_status kolibri_expert_combine(const float *y_perm, const flo
  *           [ (1 - sigma(z_te)) with sigmoid scores ]
  * (the counts carry no gradient).
  *   z           [N, E] fp32 logits, finite or -infinity; a row whose logits are
- *               all -infinity has p = 0 and gradient 0
+ *               all -infinity has p = 0 and gradient 0.  A NaN among a row's
+ *               logits makes that row's gradient and its sequence's P and loss
+ *               NaN, nothing else.
  *   ids         [N, K] int32 as kolibri_router_topk writes them.  An id outside
  *               [0, E) is not counted and sets KOLIBRI_ERR_DEVICE in the device
  *               status word; an id that stands twice in a row counts twice.

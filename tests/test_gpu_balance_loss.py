@@ -212,6 +212,30 @@ def test_gradient_reports_bad_offsets(score):
     check_status()
 
 
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("E", [64, 68, 128, 132, 384, 388])
+def test_a_row_that_is_not_a_number_shows(E, score):
+    """NaN logits, in a whole row or at one place of it, make their sequence's loss and P and their rows' gradient NaN in
+    every form of the pass, and touch nothing else."""
+    N, K = 512, 4
+    z, ids, seq, up = _inputs(N, E, K, [0, N, N], 8)
+    clean = B.kolibri_balance_loss(z, ids, 1e-3, seq_offsets=seq[:2].contiguous(), score=score, want_gz=True)[3]
+    for cols in (slice(None), slice(5, 6)):
+        broken = z.clone()
+        broken[77, cols] = float("nan")
+        for s in (seq[:2].contiguous(), seq):              # one sequence: the small form; two: the passes
+            loss, counts, prob, gz = B.kolibri_balance_loss(broken, ids, 1e-3, seq_offsets=s, score=score, want_gz=True)
+            alone = B.kolibri_balance_loss(broken, ids, 1e-3, seq_offsets=s, score=score)
+            apart = B.kolibri_balance_loss_grad(broken, counts, K, 1e-3, seq_offsets=s, score=score)
+            assert loss[0].isnan() and prob[0].isnan().all() and alone[0][0].isnan() and alone[2][0].isnan().all()
+            assert not loss[1:].any() and not prob[1:].any()
+            for t in (gz, apart):
+                assert t[77].isnan().all()
+                keep = torch.arange(N, device="cuda") != 77
+                assert torch.equal(t[keep], clean[keep])
+    check_status()
+
+
 @pytest.mark.parametrize("N", [512, 4096])
 def test_even_loads_have_the_formulas_loss(N):
     """Every expert equally loaded: f = 1, so L = lambda and the gradient vanishes, exactly."""
