@@ -236,6 +236,28 @@ def test_a_row_that_is_not_a_number_shows(E, score):
     check_status()
 
 
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("N", [64, 1100])
+def test_rows_far_from_zero_keep_their_bar(score, N):
+    """Rows far below and above zero are held to the gradient's bar itself: the row's maximum (zero, for sigmoid scores of
+    positive logits) is taken off before the exponential, so only z - c counts there.
+
+    |z - c| is below 32 and exact but for one rounding; its product with log2 e (whose constant is half a step off too) has
+    2^-23 of at most 47, the exponential 2^-22: together under 2^-17 relative.  p carries that twice, with its additions and
+    the reciprocal under 2^-16, and the bracket with it stays inside the 2^-15 of the head of this file.  With sigmoid scores
+    the row at +80 has scores of 1, so p has its additions' 2^-19 only, and a slope from exp(-z) with 2^-23 * 130 * ln 2,
+    under 2^-16; one below the normal numbers is flushed, which is less than the bar's 1e-37."""
+    E, K = 128, 4
+    z, ids, seq, up = _inputs(N, E, K, [0, N], 5)
+    z[7] -= 300.0
+    z[9] -= 3000.0
+    z[11] += 80.0
+    want = _plain(z, ids, 1.0, [0, N], score, up)
+    gz = B.kolibri_balance_loss(z, ids, 1.0, seq_offsets=seq, score=score, grad_loss=up, want_gz=True)[3]
+    err = (gz.double() - want["gz"]).abs()
+    assert (err <= want["gbar"]).all(), float((err / want["gbar"]).max())
+
+
 @pytest.mark.parametrize("N", [512, 4096])
 def test_even_loads_have_the_formulas_loss(N):
     """Every expert equally loaded: f = 1, so L = lambda and the gradient vanishes, exactly."""
