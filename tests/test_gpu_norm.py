@@ -120,6 +120,41 @@ def test_residual_that_cancels():
     _check_forward(x, res, w, EPS, out)
 
 
+@pytest.mark.parametrize("wt", [FP, BF])
+def test_eight_bit_values_are_those_of_the_quotient(wt):
+    """h = 1 and eps = 0, so y is the weight itself: y8 has to be e4m3(y / scale), scale = amax / 448, each one rounding.
+
+    The weights stand at the midpoints between e4m3 values times the group's scale and just beside them, where any other
+    order of the roundings is off by a whole step."""
+    d = 16384
+    g = torch.Generator().manual_seed(17)
+    top = torch.exp(3.0 * torch.randn(d // 128, 1, generator=g)).to(wt).float()
+    s = top / 448.0
+    grid = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()       # the values 0 .. 448
+    mid = (grid[:-1] + grid[1:]) / 2
+    v = s * mid[torch.randint(0, 126, (d // 128, 128), generator=g)] * torch.where(torch.rand(d // 128, 128, generator=g) < 0.5, -1.0, 1.0)
+    v = torch.where(torch.rand(v.shape, generator=g) < 0.3, torch.nextafter(v, 2 * v), v)
+    v[:, :1] = top
+    v[:, 1], v[:, 2] = 0.0, -0.0
+    w = v.reshape(d).to(wt)
+    v = w.float().view(-1, 128)
+    assert torch.equal(v.abs().amax(1, keepdim=True), top)
+    want = (v / s).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(d)
+    x = torch.ones(3, d, device="cuda")
+    _, y, y8, scales = B.kolibri_rms_norm(x, w.cuda(), 0.0, want_fp8=True)
+    for row in range(3):
+        assert torch.equal(y[row].cpu(), w.to(BF))                    # so y is the weight
+        assert torch.equal(scales[row].cpu(), s.view(-1))
+        assert torch.equal(y8[row].cpu().view(torch.uint8), want.view(torch.uint8))
+    # an infinite value: its group's scale is infinite, the others' quotients are 0; the groups beside it are as before
+    w[130] = torch.inf
+    _, _, y8, scales = B.kolibri_rms_norm(x, w.cuda(), 0.0, want_fp8=True)
+    q = y8[0].float().cpu()
+    assert scales[0, 1].isinf() and q[130].isnan() and not q[128:130].any() and not q[131:256].any()
+    q = y8[0].cpu().view(torch.uint8)
+    assert torch.equal(q[:128], want.view(torch.uint8)[:128]) and torch.equal(q[256:], want.view(torch.uint8)[256:])
+
+
 @pytest.mark.parametrize("N", [1, 3000])
 def test_in_place(N):
     x, res, w = _inputs(N, 2560, BF, BF, BF, 8)
