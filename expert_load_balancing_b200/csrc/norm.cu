@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "launch.h"
@@ -401,6 +402,7 @@ RowPlan row_plan(int nvec, int64_t N, bool grad) {
 }
 
 constexpr int kNormGradBlocksPerSm = 6;
+constexpr int kKnownDevices = 16;        // devices whose answers are kept; others are asked every time
 
 unsigned row_grid(int64_t N, int threads, int per_sm) {
   const int fit = 2048 / threads;
@@ -423,27 +425,37 @@ void launch_norm_x(const NormParams& p, int res_type, cudaStream_t s) {
   else launch_norm_c<XT, float>(p, s);
 }
 
-// One wave: as many blocks as are resident at once, at most `grid`.
+// One wave: as many blocks as are resident at once, at most `grid`, which is set to what was launched.  The number per SM
+// is asked for once per device and block size (of this kernel); host threads that ask at once store the same answer.
 template <typename GT, typename HT, int C, bool kRes, int kThreads>
-unsigned launch_norm_grad_t(const NormGradParams& p, int threads, unsigned grid, cudaStream_t s) {
-  static int per_sm[kMaxNormThreads / 32 + 1];
+cudaError_t launch_norm_grad_t(const NormGradParams& p, int threads, unsigned& grid, cudaStream_t s) {
+  static std::atomic<int> known[kKnownDevices][kMaxNormThreads / 32 + 1];
   auto kern = rms_norm_grad_kernel<GT, HT, C, kRes, kThreads>;
-  int& n = per_sm[threads / 32];
-  if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess || n < 1)) n = 1;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  std::atomic<int>* const slot = dev < kKnownDevices ? &known[dev][threads / 32] : nullptr;
+  int n = slot ? slot->load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0);
+    if (err != cudaSuccess) return err;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    if (slot) slot->store(n, std::memory_order_relaxed);
+  }
   const unsigned most = static_cast<unsigned>(n * device_sm_count());
   if (grid > most) grid = most;
   kern<<<grid, threads, 0, s>>>(p);
-  return grid;
+  return cudaGetLastError();
 }
 template <typename GT, typename HT, bool kRes>
-unsigned launch_norm_grad_c(const NormGradParams& p, const RowPlan& rp, unsigned grid, cudaStream_t s) {
+cudaError_t launch_norm_grad_c(const NormGradParams& p, const RowPlan& rp, unsigned& grid, cudaStream_t s) {
   if (rp.c == 1) return launch_norm_grad_t<GT, HT, 1, kRes, 512>(p, rp.threads, grid, s);
   if (rp.threads <= 256) return launch_norm_grad_t<GT, HT, 2, kRes, 256>(p, rp.threads, grid, s);
   if (rp.threads <= 512) return launch_norm_grad_t<GT, HT, 2, kRes, 512>(p, rp.threads, grid, s);
   return launch_norm_grad_t<GT, HT, 2, kRes, kMaxNormThreads>(p, rp.threads, grid, s);
 }
 template <typename GT, typename HT>
-unsigned launch_norm_grad_r(const NormGradParams& p, const RowPlan& rp, unsigned grid, cudaStream_t s) {
+cudaError_t launch_norm_grad_r(const NormGradParams& p, const RowPlan& rp, unsigned& grid, cudaStream_t s) {
   return p.gres ? launch_norm_grad_c<GT, HT, true>(p, rp, grid, s) : launch_norm_grad_c<GT, HT, false>(p, rp, grid, s);
 }
 
@@ -494,14 +506,14 @@ cudaError_t launch_rms_norm_grad(const void* gy, int gy_type, const void* h, int
   p.eps = eps;
   const RowPlan rp = row_plan(p.nvec, N, true);
   unsigned grid = row_grid(N, rp.threads, kNormGradBlocksPerSm);      // as the workspace was sized, at most
+  cudaError_t err;
   if (gy_type == KOLIBRI_TYPE_BF16) {
-    if (h_type == KOLIBRI_TYPE_BF16) grid = launch_norm_grad_r<__nv_bfloat16, __nv_bfloat16>(p, rp, grid, s);
-    else grid = launch_norm_grad_r<__nv_bfloat16, float>(p, rp, grid, s);
+    if (h_type == KOLIBRI_TYPE_BF16) err = launch_norm_grad_r<__nv_bfloat16, __nv_bfloat16>(p, rp, grid, s);
+    else err = launch_norm_grad_r<__nv_bfloat16, float>(p, rp, grid, s);
   } else {
-    if (h_type == KOLIBRI_TYPE_BF16) grid = launch_norm_grad_r<float, __nv_bfloat16>(p, rp, grid, s);
-    else grid = launch_norm_grad_r<float, float>(p, rp, grid, s);
+    if (h_type == KOLIBRI_TYPE_BF16) err = launch_norm_grad_r<float, __nv_bfloat16>(p, rp, grid, s);
+    else err = launch_norm_grad_r<float, float>(p, rp, grid, s);
   }
-  cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || !gweight) return err;
   return launch_pdl(norm_weight_sum_kernel, dim3((d + 31) / 32), dim3(32, 32), 0, s, dim3(0, 0, 0),
                     static_cast<const float*>(p.part), static_cast<int>(grid), static_cast<int>(d), gweight);

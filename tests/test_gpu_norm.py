@@ -12,6 +12,7 @@ Bars.  Half a rounding step is 2^-8 (bf16), 2^-24 (fp32), 2^-4 (e4m3, and
   of their terms' magnitudes: 2^-17 (|r t| + |h| r^3 mean|t h|).
 - gweight sums N terms in fp32: (N + 64) 2^-24 + 2^-17 of the sum of magnitudes."""
 import math
+import threading
 
 import pytest
 import torch
@@ -331,6 +332,42 @@ def test_other_stream_and_graph():
     for _ in range(2):
         graph.replay()
     same()
+    check_status()
+
+
+def test_gradient_from_several_host_threads():
+    """Four threads, a stream and buffers each, on sizes that no test before has launched: the bits of calls one by one."""
+    shapes = [(1200, 328), (1200, 2456), (1200, 3352), (700, 4632), (1100, 6536), (1100, 12296)]
+    cases = []
+    for i, (N, d) in enumerate(shapes):
+        h, _, w = _inputs(N, d, FP, None, BF, 60 + i)
+        cases.append((_randn(torch.Generator(device="cuda").manual_seed(i), N, d), h, w))
+    torch.cuda.synchronize()
+    got, wrong = {}, []
+    start = threading.Barrier(4)
+
+    def work(t):
+        try:
+            st = torch.cuda.Stream()
+            start.wait()
+            for i, (gy, h, w) in enumerate(cases):
+                got[t, i] = B.kolibri_rms_norm_grad(gy, h, w, EPS, stream=st)
+            st.synchronize()
+        except Exception as e:                      # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    torch.cuda.synchronize()
+    for i, (gy, h, w) in enumerate(cases):
+        gx, gg = B.kolibri_rms_norm_grad(gy, h, w, EPS)
+        _check_grad(gy, h, w, EPS, None, gx, gg)
+        for t in range(4):
+            assert torch.equal(got[t, i][0], gx) and torch.equal(got[t, i][1], gg), (t, i)
     check_status()
 
 
