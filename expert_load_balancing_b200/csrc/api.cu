@@ -1,5 +1,6 @@
 // api.cu -- the extern "C" boundary declared in include/kolibri_router.h:
 // argument validation, workspace sizing and the device status word.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -421,6 +422,10 @@ kolibri_status kolibri_expert_combine(const float* y_perm, const float* y_shared
 
 namespace {
 
+// Units with a status word of their own that have been launched: only theirs are read by kolibri_device_status (14 us
+// each).  Never cleared, since a captured graph may launch them at any time.
+std::atomic<bool> g_loss_used{false}, g_expert_fp8_used{false};
+
 kolibri_status check_balance_loss(int64_t N, int32_t E, int32_t K, int32_t S, const int64_t* seq, int32_t score,
                                   int32_t accumulate, double lambda) {
   const kolibri_status st = check_ek(N, E, K);
@@ -463,6 +468,7 @@ kolibri_status kolibri_balance_loss(const float* z, const int32_t* ids, const in
                         static_cast<const void*>(prob), static_cast<const void*>(gz), static_cast<const void*>(ws)})
     if (!aligned16(q)) return KOLIBRI_ERR_INVALID_ARG;
   if (ws_bytes < need) return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
+  g_loss_used.store(true);
   return from_cuda(launch_balance_loss(z, ids, seq_offsets, N, E, K, S, score, lambda, grad_loss, accumulate, loss,
                                        counts, prob, gz, ws, static_cast<cudaStream_t>(stream)));
 }
@@ -475,6 +481,7 @@ kolibri_status kolibri_balance_loss_grad(const float* z, const int32_t* counts, 
   if (!z || !counts || !gz) return KOLIBRI_ERR_INVALID_ARG;
   if (!aligned16(z) || !aligned16(counts) || !aligned16(seq_offsets) || !aligned16(grad_loss) || !aligned16(gz))
     return KOLIBRI_ERR_INVALID_ARG;
+  g_loss_used.store(true);
   return from_cuda(launch_balance_loss_grad(z, counts, seq_offsets, N, E, K, S, score, lambda, grad_loss, accumulate,
                                             gz, static_cast<cudaStream_t>(stream)));
 }
@@ -543,6 +550,7 @@ kolibri_status kolibri_expert_ffn_fp8(const void* x8, const float* x_scale, cons
   if (ws_bytes < expert_fp8_ws_bytes(N, d, F, K, shared)) return KOLIBRI_ERR_WORKSPACE_TOO_SMALL;
   const ExpertFp8Args a{x8, x_scale, perm, offsets, inv, gates, w_gate_up, s_gate_up, w_down, s_down, ws_gate_up,
                         ss_gate_up, ws_down, ss_down, y, N, d, F, E, K, ws};
+  g_expert_fp8_used.store(true);
   return from_cuda(launch_expert_ffn_fp8(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -555,11 +563,12 @@ kolibri_status kolibri_selftest_bounded_wait(uint64_t limit_ns, void* stream) {
 kolibri_status kolibri_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return KOLIBRI_ERR_CUDA;
-  const unsigned v = status_take_api() | status_take_eqb() | status_take_noalloc() |
-                     status_take_permute() | status_take_route() | status_take_logits() |
-                     status_take_forward() | status_take_balance() | status_take_small() |
-                     status_take_experts() | status_take_decode() | status_take_balance_loss() |
-                     status_take_expert_fp8() | status_take_expert_fp8_decode();
+  unsigned v = status_take_api() | status_take_eqb() | status_take_noalloc() |
+               status_take_permute() | status_take_route() | status_take_logits() |
+               status_take_forward() | status_take_balance() | status_take_small() |
+               status_take_experts() | status_take_decode();
+  if (g_loss_used.load()) v |= status_take_balance_loss();
+  if (g_expert_fp8_used.load()) v |= status_take_expert_fp8() | status_take_expert_fp8_decode();
   if (v & kStatusReadFailed) return KOLIBRI_ERR_CUDA;
   if (v & kStatusTimeout) return KOLIBRI_ERR_TIMEOUT;
   if (v & kStatusBadInput) return KOLIBRI_ERR_DEVICE;
