@@ -125,33 +125,30 @@ __device__ __forceinline__ void block_sums(float (&v)[NV], float* buf, int warps
   }
 }
 
-// y / s of two values from q = 1 / s rounded to nearest: t = y q is within a unit of the quotient, its remainder t s - y is
-// exact, and the step along it rounds to the quotient's nearest (Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990, theorem 3).  y q alone is one rounding more, and at a midpoint of e4m3 that is
-// a whole step of y8.  The remainder's sign is the one that keeps a quotient of -0.  Two values per instruction: 16,384
-// rows of 2560 take 64.8 us (y q alone 65.6, the same steps one by one 67.6, a division each 72.8).  Two ends: below a
-// scale of 1e-28 the remainder may round, which a quotient within 2^-7 units of a boundary would show; an infinite scale
-// leaves 0 for what is finite, as a division does.
+// y / s for two values per instruction, with 1 / s = hi + lo: hi rounded down, so that lo >= 0 and a quotient of -0 keeps its
+// sign, lo = (1 - s hi) hi with the bracket exact.  y lo + y hi is within 2^-45 of the quotient before its one rounding,
+// so it rounds as the quotient does unless that lies within 2^-21 units of a boundary.  y (448 / amax) is one rounding
+// more, and at a midpoint of e4m3 that is a whole step of y8.  16,384 rows of 2560, in a graph: 62.2 us (61.7 with y (448 /
+// amax), 63.6 with a step along the remainder y - t s instead, 7 more with a division each).  An infinite scale leaves
+// 0 for what is finite, as a division does; above a scale of 1e30 lo is subnormal and has fewer bits.
 struct Quotient {
-  uint64_t s, q, nq, minus;
+  uint64_t hi, lo;
   __device__ __forceinline__ static uint64_t twice(float f) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(f));
     return r;
   }
   __device__ __forceinline__ explicit Quotient(float scale) {
-    const float r = __frcp_rn(scale);
-    s = twice(r > 0.0f ? scale : 0.0f);          // no infinity times 0
-    q = twice(r);
-    nq = twice(-r);
-    minus = twice(-1.0f);
+    const float r = __frcp_rd(scale);
+    hi = twice(r);
+    lo = twice(r > 0.0f ? __fmaf_rn(-scale, r, 1.0f) * r : 0.0f);
   }
   __device__ __forceinline__ float2 of(float y0, float y1) const {
     float2 o;
-    asm("{\n\t.reg .b64 y, m, t, r;\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 m, y, %7;\n\tmul.rn.f32x2 t, y, %5;\n\t"
-        "fma.rn.f32x2 r, t, %4, m;\n\tfma.rn.f32x2 r, r, %6, t;\n\tmov.b64 {%0, %1}, r;\n\t}"
+    asm("{\n\t.reg .b64 y, t;\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 t, y, %5;\n\t"
+        "fma.rn.f32x2 t, y, %4, t;\n\tmov.b64 {%0, %1}, t;\n\t}"
         : "=f"(o.x), "=f"(o.y)
-        : "f"(y0), "f"(y1), "l"(s), "l"(q), "l"(nq), "l"(minus));
+        : "f"(y0), "f"(y1), "l"(hi), "l"(lo));
     return o;
   }
 };
