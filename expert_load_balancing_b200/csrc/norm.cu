@@ -13,11 +13,11 @@
 //
 // Bound by HBM: each input is read once and each output written once, the
 // row stays in registers between the sum of squares and the outputs.  Measured:
-// 16,384 rows of 2560 (bf16 in, residual, bf16 and 8-bit out, 379 MB) 63 us, 0.92
+// 16,384 rows of 2560 (bf16 in, residual, bf16 and 8-bit out, 379 MB) 62 us, 0.94
 // of a copy's bandwidth; 65,536 rows of 2048 (fp32 residual, 1.61 GB) 236 us,
-// 1.04; the gradient of 16,384 rows of 2560 (335 MB) 57 us and 4 for the weight's
-// sum, 0.90; a row of one token 4.2 us in a graph, the latency of two dependent
-// reads and a block's sum.
+// 1.04; the gradient of 16,384 rows of 2560 (335 MB) 58 us, 0.89, and 4 for the
+// weight's sum; a row of one token 4.2 us in a graph of its own, the latency of a
+// launch, one round of reads (none waits for another) and a block's sum.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "launch.h"
+#include "approx.cuh"
 #include "common.cuh"
 #include "pdl.cuh"
 
@@ -37,7 +38,6 @@ constexpr int kGroupVecs = 128 / kVec;   // threads of one 8-bit scale group
 constexpr int kMaxNormThreads = 1024;   // d = 16384 at two vecs per thread
 constexpr int kMaxNormWarps = kMaxNormThreads / 32;
 constexpr float kAmaxMin = 1e-30f;       // keeps the scale and its reciprocal normal numbers
-constexpr float kE4m3Max = 448.0f;
 
 struct Vec8 {
   float v[kVec];
@@ -125,12 +125,20 @@ __device__ __forceinline__ void block_sums(float (&v)[NV], float* buf, int warps
   }
 }
 
-// y / s for two values per instruction, with 1 / s = hi + lo: hi rounded down, so that lo >= 0 and a quotient of -0 keeps its
-// sign, lo = (1 - s hi) hi with the bracket exact.  y lo + y hi is within 2^-45 of the quotient before its one rounding,
-// so it rounds as the quotient does unless that lies within 2^-21 units of a boundary.  y (448 / amax) is one rounding
-// more, and at a midpoint of e4m3 that is a whole step of y8.  16,384 rows of 2560, in a graph: 62.2 us (61.7 with y (448 /
-// amax), 63.6 with a step along the remainder y - t s instead, 7 more with a division each).  An infinite scale leaves
-// 0 for what is finite, as a division does; above a scale of 1e30 lo is subnormal and has fewer bits.
+// a / 448 rounded to nearest, from 1 / 448 in two parts (hi rounded down): a hi + a lo is within 2^-46 of the quotient
+// before its one rounding, and a quotient by 7 lies 1/14 of a unit or more from a boundary, if it is not one of the numbers.
+__device__ __forceinline__ float over_448(float a) {
+  constexpr float kHi = 0x1.249248p-9f, kLo = 0x1.24924ap-33f;
+  return __fmaf_rn(a, kHi, __fmul_rn(a, kLo));
+}
+
+// y / s for two values per instruction, with 1 / s = hi + lo.  hi is the hardware's reciprocal taken down by 2^-22, more than
+// its error, so that lo > 0 and a quotient of -0 keeps its sign; with e = 1 - s hi, lo = hi (e + e^2).  y lo + y hi is
+// within 2^-43 of the quotient before its one rounding, so it rounds as the quotient does unless that lies within
+// 2^-19 units of a boundary.  y (448 / amax) is one rounding more, and at a midpoint of e4m3 that is a whole step
+// of y8.  16,384 rows of 2560, in a graph: 61.6 us (61.7 with y (448 / amax), 62.1 with the reciprocal and the scale rounded by
+// the compiler's functions, 63.6 with a step along the remainder y - t s, 7 more with a division each).  An infinite
+// scale leaves 0 for what is finite, as a division does; above a scale of 1e30 lo is subnormal and has fewer bits.
 struct Quotient {
   uint64_t hi, lo;
   __device__ __forceinline__ static uint64_t twice(float f) {
@@ -138,10 +146,10 @@ struct Quotient {
     asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(f));
     return r;
   }
-  __device__ __forceinline__ explicit Quotient(float scale) {
-    const float r = __frcp_rd(scale);
+  __device__ __forceinline__ explicit Quotient(float s) {
+    const float r = rcp_fast(s) * (1.0f - 0x1p-22f), e = __fmaf_rn(-s, r, 1.0f);
     hi = twice(r);
-    lo = twice(r > 0.0f ? __fmaf_rn(-scale, r, 1.0f) * r : 0.0f);
+    lo = twice(r > 0.0f ? __fmaf_rn(e, e, e) * r : 0.0f);
   }
   __device__ __forceinline__ float2 of(float y0, float y1) const {
     float2 o;
@@ -230,7 +238,7 @@ __global__ void __launch_bounds__(C == 1 ? 512 : kMaxNormThreads) rms_norm_kerne
 #pragma unroll
       for (int o = kGroupVecs / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
       a = fmaxf(a, kAmaxMin);
-      const float s = __fdiv_rn(a, kE4m3Max);
+      const float s = over_448(a);
       const Quotient by(s);
       uint32_t w[2];
 #pragma unroll
@@ -389,8 +397,9 @@ struct RowPlan {
   int c, threads;
 };
 // One vec each while a block's threads suffice: 16,384 rows of 2560 take the
-// norm 63.5 us at one, 70 at two.  The gradient keeps a row and the next one in
-// flight and rather has two (56.5 us, 62 at one) unless there are few rows.
+// norm 62 us at one, 71 at two.  The gradient keeps a row and the next one in
+// flight and rather has two (57.6 us, 63.5 at one) unless there are few rows
+// (1100: 10.8 us with the weight's sum, 10.1 at one; 2000: 13.8 and 13.3).
 RowPlan row_plan(int nvec, int64_t N, bool grad) {
   RowPlan rp;
   rp.c = nvec > 512 || (grad && nvec > 64 && N > 1024) ? 2 : 1;
