@@ -179,8 +179,9 @@ struct LossParams {
 // and gradient: 575 us at four blocks, 640 at two, 765 at the three of an
 // unbounded register count).  With four float4s a lane the sums and logits need
 // more than the 64 registers of four blocks, and two without spills beat three
-// with (E = 128, 65,536 rows in 61 sequences, loss and then gradient, in a graph:
-// 32.8 us, 36.9).
+// with at every such width (262,144 rows, sigmoid scores, loss and gradient at
+// once, in a graph: E = 128 64 us at two and 91 at three, 256 105 and 155, 512 188
+// and 308; E = 128, 65,536 rows in 61 sequences, loss and then gradient: 34 and 38).
 template <int V>
 struct LossBlocks {
   static constexpr int kPerSm = V <= 3 ? 4 : 2;
@@ -469,9 +470,10 @@ __global__ void __launch_bounds__(32 * kFinishRows) balance_finish_kernel(const 
 // A small batch of one sequence: one launch, a cluster of eight blocks that
 // hold the counts and the shares of P in shared memory and read one another's.
 // The launches of the other form cost 12.3 us whatever the size; 256 rows of 384
-// take 7.2 here (9.0 with eight warps), 64 rows 5.6 (in a graph).  Eight SMs
-// cannot carry more: 680 rows of 384 12.5 (14.4 the other way), 1024 16.4 (13.5);
-// 512 rows of 512 12.0 (14.1), 1024 of 256 12.3 (12.4).
+// take 7.3 here (9.0 with eight warps; 13.4 the other way), 64 rows 5.4 (in a graph
+// of fifty calls, each on inputs of its own).  Eight SMs cannot carry more: 680 rows
+// of 384 14.5 (14.8 the other way), 1024 18.9 (14.4); 512 rows of 512 12.4 (15.7),
+// 1024 of 256 11.8 (15.3).
 constexpr int kClusterBlocks = 8;
 constexpr int64_t kSmallRows = 1024;
 constexpr int64_t kSmallLogits = 1 << 18;

@@ -5,7 +5,7 @@
 // 128 x 128 block, activations with one per 1 x 128 group; the router stays
 // bf16.  For slot p of expert e and token t:
 //   g, u  = sum over k blocks b of  xs[t,b] ws[e,.,b] (sum_{k in b} x8 w8)    fp32
-//   h     = SiLU(g) u, then per 128 units hs = max(amax|h|, 1e-30) / 448, h8 = e4m3(h / hs)
+//   h     = SiLU(g) u, then per 128 units hs = max(amax|h|, 1e-30) / 448, h8 = e4m3(h 448 / max(amax|h|, 1e-30))
 //   o[p]  = sum over unit blocks b of  hs[p,b] wds[e,.,b] (sum h8 wd8)        fp32, kept in fp16 (below)
 //   y[t]  = o_shared[t] + sum_k gates[t,k] o[inv[t K + k]]                    fp32, rounded to bf16
 //
@@ -178,8 +178,9 @@ constexpr uint32_t make_idesc_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// SiLU(g) u: a few fp32 units off, far below the step of e4m3.  g far below
-// zero gives -0 (the exponential overflows, its reciprocal is 0).
+// SiLU(g) u: a few fp32 units off, far below the step of e4m3 (and more than the
+// one rounding by which h (448 / amax) differs from the quotient by the scale).  g
+// far below zero gives -0 (the exponential overflows, its reciprocal is 0).
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * rcp_fast(1.0f + exp2_fast(g * -kLog2e)) * u;
 }

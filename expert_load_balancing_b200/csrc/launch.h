@@ -207,9 +207,12 @@ size_t expert_fp8_ws_bytes(int64_t N, int32_t d, int32_t F, int32_t K, bool shar
 cudaError_t launch_expert_ffn_fp8(const ExpertFp8Args& a, cudaStream_t s);
 // Few tokens (expert_fp8_decode.cu): up to this many rows, shared ones included.
 // The streaming form reads an expert's weights once per row, the tiles once per
-// expert and 128 rows, in four launches.  d = 2560, F = 512, 6 of 384 experts and
-// the shared one, weights not in L2: 56 rows 64.5 us by rows, 70.7 by tiles; 112
-// rows 111 and 97.
+// expert and 128 rows, in four launches.  d = 2560, F = 512, weights not in L2, us by
+// rows and by tiles: 6 of 384 experts and the shared one, where nearly every row has
+// an expert of its own, 7 rows 12.4 and 30.8, 63 rows 63.6 and 59.5, 112 rows 108
+// and 80.  Where experts are few the tiles gain earlier, which this rule, on rows
+// alone, does not see: 2 of 8 and the shared one, 12 rows 15.5 and 27.8, 24 rows 23.6
+// and 28.9, 48 rows 38.3 and 30.3; 2 of 8, 64 rows 51.9 and 30.6.
 constexpr int64_t kFp8DecodeSlots = 64;
 bool expert_fp8_decode_preferred(int64_t N, int32_t K, bool shared);
 cudaError_t launch_expert_ffn_fp8_decode(const ExpertFp8Args& a, cudaStream_t s);

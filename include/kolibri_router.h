@@ -602,7 +602,9 @@ KOLIBRI_API kolibri_status kolibri_balance_loss_grad(const float *z, const int32
  * types agree (in place); outputs must not overlap otherwise.
  * d % 8 == 0, 8 <= d <= 16384, eps >= 0 (a row of zeros with eps = 0 is not a
  * number).  The squares are summed in fp32: a row whose sum of h^2 leaves fp32's
- * range (|h| about 1e19) has y = 0.
+ * range (|h| about 1e19) has y = 0, and with eps = 0 a row of |h| below about 1e-19
+ * loses bits, down to not a number.  y / scale is the fp32 quotient rounded to
+ * nearest (short of 2^-19 units beside a boundary; amax below 1e33).
  */
 KOLIBRI_API kolibri_status kolibri_rms_norm(const void *x, int32_t x_type, const void *res,
                                             int32_t res_type, const void *weight,
@@ -620,7 +622,8 @@ KOLIBRI_API kolibri_status kolibri_rms_norm(const void *x, int32_t x_type, const
  *   gweight [d] fp32, written if not NULL; ws then has
  *        kolibri_rms_norm_grad_workspace_size(N, d) bytes, 16-byte aligned
  *        (need not be initialised; may be NULL without gweight).
- * Sums in fp32 in a fixed order.  Shapes as kolibri_rms_norm.
+ * Sums in fp32 in a fixed order: gx is right wherever the forward's y is, as long
+ * as the sum of gy weight h stays in fp32's range.  Shapes as kolibri_rms_norm.
  */
 KOLIBRI_API size_t kolibri_rms_norm_grad_workspace_size(int64_t N, int32_t d);
 KOLIBRI_API kolibri_status kolibri_rms_norm_grad(const void *gy, int32_t gy_type, const void *h,
