@@ -285,7 +285,7 @@ struct NormGradParams {
 // The next row's inputs are loaded before this row is reduced, and both rows
 // stay as they lie in memory until they are used: with each row's loads behind
 // the last one's barrier 16,384 rows of 2560 (bf16, gres) took 101 us, with both
-// rows held in fp32 89, so 56.5.
+// rows held in fp32 89, so 57.5.
 template <typename GT, typename HT, int C, bool kRes, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads <= 256 ? 2 : 1) rms_norm_grad_kernel(const NormGradParams p) {
   constexpr bool kAhead = kThreads <= 512;      // rows above 8192 columns: no registers for a second one
